@@ -372,6 +372,117 @@ DSA_API dsa_status dsa_indexer_backward(const dsa_shape* shape, const uint8_t* q
                                 int q_begin, int q_count, float* dq, float* dw,
                                 float* dk, void* stream);
 
+/* ---- Rows around the path: norm and rotation, the 8-bit caches --------------
+ * Additions of this library (the pages start from prepared operands): what a
+ * layer does to its queries and keys before the path, and a latent cache of
+ * half the size.  A step runs dsa_norm_rope -> dsa_cache_write -> dsa_forward8
+ * (or dsa_indexer_scores, dsa_topk, dsa_sparse_attn8).  Positions, seqlens and
+ * paged caches as above; a length outside [T, S] or an unmapped page that is
+ * needed is reported on the device. */
+
+/* Rows of dsa_norm_rope: H heads of D columns each, for queries and keys.
+ * Limits: D a multiple of 8, at most 1024; norm_cols a multiple of 8;
+ * rope_cols a multiple of 16, at most 256; at most 1024 heads a side. */
+typedef struct {
+  int Hq, Hk;             /* query heads and key heads of a token (0: side absent) */
+  int D;                  /* columns of a head row                            */
+  int norm_cols;          /* leading columns that are normalised (0: none)    */
+  int rope_cols;          /* trailing columns that are rotated (0: none)      */
+  int interleaved;        /* rotated pairs (2i, 2i+1) instead of (i, i + rope_cols/2) */
+  float eps;              /* >= 0, added to the mean square                   */
+  const float* q_weight;  /* device FP32 [norm_cols], 16-byte aligned, or NULL (ones) */
+  const float* k_weight;  /* the same for keys                                */
+  const float* inv_freq;  /* device FP32 [rope_cols/2]: radians per position  */
+} dsa_norm_rope_desc;
+
+/* RMS norm of every head row and its rotation by position, in one pass.
+ *   q [B, T, Hq, D], k [B, T, Hk, D] BF16 -> q_out, k_out (the input buffer
+ *   itself is allowed, any other overlap is not).
+ *   z_c = weight_c x_c / sqrt(mean_{c < norm_cols} x_c^2 + eps) for
+ *   c < norm_cols, x_c past them; the last rope_cols columns of z are rotated
+ *   in pairs (a, b) -> (a cos - b sin, a sin + b cos) by pos(t) inv_freq_i
+ *   (the angle is formed in FP64); rounded to BF16 once. */
+DSA_API dsa_status dsa_norm_rope(const dsa_shape* shape, const dsa_norm_rope_desc* desc, const uint16_t* q,
+                         const uint16_t* k, uint16_t* q_out, uint16_t* k_out, void* stream);
+
+/* Workspace of dsa_norm_rope_backward; 0 if the arguments are invalid. */
+DSA_API size_t dsa_norm_rope_workspace_size(const dsa_shape* shape, const dsa_norm_rope_desc* desc);
+
+/* Gradients of dsa_norm_rope: from its inputs q, k (not needed and may be
+ * NULL when norm_cols is 0) and the gradients dq_out, dk_out of its outputs,
+ * dq, dk BF16 (dq_out's and dk_out's own buffers are allowed) and the norm
+ * weights' dq_weight, dk_weight FP32 [norm_cols] (written, not added to;
+ * NULL: not wanted).  The weight sums run in a fixed order.
+ * ws: dsa_norm_rope_workspace_size bytes (may be NULL when no weight gradient
+ * is wanted). */
+DSA_API dsa_status dsa_norm_rope_backward(const dsa_shape* shape, const dsa_norm_rope_desc* desc, const uint16_t* q,
+                                  const uint16_t* k, const uint16_t* dq_out, const uint16_t* dk_out, uint16_t* dq,
+                                  uint16_t* dk, float* dq_weight, float* dk_weight, void* ws, size_t ws_bytes,
+                                  void* stream);
+
+/* Quantises a step's new rows and writes them to their places, in one launch.
+ *   kv [B, T, d_k] BF16 -> kv8 (e4m3 bytes) and kv_scale (FP32), caches laid
+ *   out as kv with one scale per row: row of position pos(t);
+ *   k_I [B, T, D_I] BF16 -> kI8, kI_scale: the k_I and k_scale of dsa_inputs;
+ *   q_I [B, T, H_I, D_I] BF16 -> qI8, qI_scale [B, T, H_I]: its q_I, q_scale.
+ * Each of the three parts may be left out (its three pointers NULL).
+ * A row's scale is 2^e with the smallest e >= -48 for which
+ * max|x| <= 448 * 2^e, its bytes are e4m3(x * 2^-e) rounded to nearest even
+ * (values past 240 * 2^120 are stored as that; x holds no NaN).  Other rows of the caches are left as they are; a row whose
+ * page is unmapped is reported and dropped. */
+DSA_API dsa_status dsa_cache_write(const dsa_shape* shape, const uint16_t* kv, uint8_t* kv8, float* kv_scale,
+                           const uint16_t* k_I, uint8_t* kI8, float* kI_scale, const uint16_t* q_I, uint8_t* qI8,
+                           float* qI_scale, void* stream);
+
+/* Reads tokens [s_begin, s_begin + s_count) of every sequence back:
+ *   kv [B, s_count, d_k], k_I [B, s_count, D_I] BF16 = byte * scale, rounded
+ *   to nearest even (exact for dsa_cache_write's scales).
+ * Either part may be left out.  Rows of tokens at or past L_b are left as
+ * they are; a row of an unmapped page is reported and zeroed. */
+DSA_API dsa_status dsa_cache_read(const dsa_shape* shape, int s_begin, int s_count, const uint8_t* kv8,
+                          const float* kv_scale, uint16_t* kv, const uint8_t* kI8, const float* kI_scale,
+                          uint16_t* k_I, void* stream);
+
+/* Bytes of workspace for dsa_sparse_attn8, dsa_dense_attn8 and dsa_forward8
+ * (16-byte aligned).  0 if the shape is invalid. */
+DSA_API size_t dsa_workspace8_size(const dsa_shape* shape);
+
+/* Step C over an 8-bit cache: dsa_sparse_attn with key row s dequantised as
+ * kv_scale[s] * e4m3(kv8[s]) (V = its first d_v columns).  kv8 [B, S, d_k]
+ * bytes and kv_scale [B, S] FP32 (paged: pools of rows); any finite scales in
+ * [2^-100, 2^100].  Selected rows hold no NaN bytes; other rows may hold
+ * anything.  The products are those of the given bytes with q split into two
+ * e4m3 terms and of the probabilities split likewise, accumulated in FP32;
+ * out is rounded to BF16 once.  The two modes give the same results; calls of
+ * few rows split their keys over the SMs and need the workspace. */
+DSA_API dsa_status dsa_sparse_attn8(const dsa_shape* shape, const uint16_t* q, const uint8_t* kv8,
+                            const float* kv_scale, const int32_t* idx, uint16_t* out, float* lse, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* dsa_dense_attn over an 8-bit cache: every query over all its visible keys. */
+DSA_API dsa_status dsa_dense_attn8(const dsa_shape* shape, const uint16_t* q, const uint8_t* kv8,
+                           const float* kv_scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/* Inputs of the whole path over an 8-bit cache (device pointers). */
+typedef struct {
+  const uint8_t* q_I;      /* as in dsa_inputs                               */
+  const float* q_scale;
+  const float* w;
+  const uint8_t* k_I;
+  const float* k_scale;
+  const uint16_t* q;
+  const uint8_t* kv8;      /* [B, S, d_k] e4m3 cached rows                    */
+  const float* kv_scale;   /* [B, S]                                          */
+} dsa_inputs8;
+
+/* dsa_forward over an 8-bit cache, in shape->mode (DSA_DECODE: T == 1).  ws:
+ * dsa_workspace8_size bytes; in prefill dsa_select_workspace_size plus what
+ * dsa_workspace8_size exceeds dsa_workspace_size by is enough, and steps A and
+ * B then run as dsa_select does. */
+DSA_API dsa_status dsa_forward8(const dsa_shape* shape, const dsa_inputs8* in, uint16_t* out, float* lse,
+                        int32_t* idx_out, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronises `stream`, then reads and clears the device error word of the
  * current device.  Returns DSA_OK, DSA_ERR_TIMEOUT or DSA_ERR_DEVICE_BOUNDS
  * (the first error recorded since the last call), or DSA_ERR_CUDA if the

@@ -362,6 +362,30 @@ dsa_status run_attn(const LaunchCtx& c, const dsa_shape* s, const uint16_t* q, c
   return from_cuda(launch_sparse_attn(c, a));
 }
 
+// The attention over an 8-bit cache: its arguments from a shape.
+Attn8Args attn8_args(const dsa_shape* s) {
+  Attn8Args a = {};
+  a.map = kv_map(s);
+  a.B = s->B; a.T = s->T; a.S = s->S; a.H = s->H; a.d_k = s->d_k; a.d_v = s->d_v; a.k = s->k;
+  a.tau = tau_of(s);
+  return a;
+}
+
+dsa_status run_attn8(const LaunchCtx& c, const dsa_shape* s, const uint16_t* q, const uint8_t* kv8,
+                     const float* kv_scale, const int32_t* idx, int dense_rows, uint16_t* out, float* lse, void* ws,
+                     size_t ws_bytes) {
+  Attn8Args a = attn8_args(s);
+  const size_t need = attn8_workspace_bytes(a, c.num_sms);
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return DSA_ERR_WORKSPACE;
+  a.q = q; a.kv8 = kv8; a.kv_scale = kv_scale; a.idx = idx; a.dense_rows = dense_rows;
+  a.out = out; a.lse = lse; a.ws = ws;
+  return from_cuda(launch_attn8(c, a));
+}
+
+bool attn8_ptrs_ok(const uint16_t* q, const uint8_t* kv8, const float* kv_scale, const uint16_t* out, const void* ws) {
+  return q && kv8 && kv_scale && out && aligned16(q) && aligned16(kv8) && aligned16(out) && aligned16(ws);
+}
+
 bool indexer_ptrs_ok(const uint8_t* q_I, const float* q_scale, const float* w, const uint8_t* k_I,
                      const float* k_scale) {
   return q_I && q_scale && w && k_I && k_scale && aligned16(q_I) && aligned16(k_I);
@@ -540,6 +564,66 @@ dsa_status dsa_decode(const dsa_shape* s, const dsa_inputs* in, uint16_t* out, f
   dsa_shape m = *s;
   m.mode = DSA_DECODE;
   return dsa_forward(&m, in, out, lse, idx_out, ws, ws_bytes, stream);
+}
+
+// Steps A and B in the score tile's workspace, the attention's own behind it.
+size_t dsa_workspace8_size(const dsa_shape* s) {
+  if (check_shape(s) != DSA_OK) return 0;
+  DeviceInfo d;
+  int dev = 0;
+  int sms = 148;
+  if (device_info(&d, &dev) == DSA_OK) sms = d.num_sms;
+  return round_up(ws_layout(s, sms, false).total, 256) + attn8_workspace_bytes(attn8_args(s), sms);
+}
+
+dsa_status dsa_sparse_attn8(const dsa_shape* s, const uint16_t* q, const uint8_t* kv8, const float* kv_scale,
+                            const int32_t* idx, uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  dsa_status st = check_shape(s);
+  if (st != DSA_OK) return st;
+  if (!attn8_ptrs_ok(q, kv8, kv_scale, out, ws) || idx == nullptr) return DSA_ERR_INVALID_ARG;
+  LaunchCtx c;
+  if ((st = make_ctx(stream, &c)) != DSA_OK) return st;
+  return run_attn8(c, s, q, kv8, kv_scale, idx, 0, out, lse, ws, ws_bytes);
+}
+
+dsa_status dsa_dense_attn8(const dsa_shape* s, const uint16_t* q, const uint8_t* kv8, const float* kv_scale,
+                           uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  dsa_status st = check_shape(s);
+  if (st != DSA_OK) return st;
+  if (!attn8_ptrs_ok(q, kv8, kv_scale, out, ws)) return DSA_ERR_INVALID_ARG;
+  LaunchCtx c;
+  if ((st = make_ctx(stream, &c)) != DSA_OK) return st;
+  return run_attn8(c, s, q, kv8, kv_scale, nullptr, 0, out, lse, ws, ws_bytes);
+}
+
+dsa_status dsa_forward8(const dsa_shape* s, const dsa_inputs8* in, uint16_t* out, float* lse, int32_t* idx_out,
+                        void* ws, size_t ws_bytes, void* stream) {
+  dsa_status st = check_shape(s);
+  if (st != DSA_OK) return st;
+  if (in == nullptr || idx_out == nullptr) return DSA_ERR_INVALID_ARG;
+  if (!indexer_ptrs_ok(in->q_I, in->q_scale, in->w, in->k_I, in->k_scale)) return DSA_ERR_INVALID_ARG;
+  if (!attn8_ptrs_ok(in->q, in->kv8, in->kv_scale, out, ws)) return DSA_ERR_INVALID_ARG;
+  if (s->mode == DSA_DECODE && s->T != 1) return DSA_ERR_INVALID_ARG;
+  LaunchCtx c;
+  if ((st = make_ctx(stream, &c)) != DSA_OK) return st;
+  // the attention's scratch lies behind the widest layout of steps A and B
+  // that the rest of the workspace holds
+  const size_t need8 = attn8_workspace_bytes(attn8_args(s), c.num_sms);
+  const size_t front = ws == nullptr || ws_bytes < need8 ? 0 : (ws_bytes - need8) / 256 * 256;
+  const WsLayout L = ws_choose(s, c.num_sms, front);
+  if (front < L.total) return DSA_ERR_WORKSPACE;
+  // rows whose visible keys all fit in k: no scores, the selection is 0..pos
+  const int d_rows = dense_rows_of(s);
+  if (d_rows > 0 &&
+      (st = run_topk(c, s, reinterpret_cast<float*>(static_cast<char*>(ws) + L.scores_off), scores_ld(s), 0, d_rows,
+                     idx_out, nullptr, 0)) != DSA_OK)
+    return st;
+  for (int q0 = d_rows; q0 < s->T; q0 += L.q_rows) {
+    const int cnt = (s->T - q0) < L.q_rows ? (s->T - q0) : L.q_rows;
+    if ((st = run_select(c, s, L, ws, in->q_I, in->q_scale, in->w, in->k_I, in->k_scale, q0, cnt, idx_out)) != DSA_OK)
+      return st;
+  }
+  return run_attn8(c, s, in->q, in->kv8, in->kv_scale, idx_out, d_rows, out, lse, static_cast<char*>(ws) + front, need8);
 }
 
 dsa_status dsa_selftest_wait_timeout(void* stream) {

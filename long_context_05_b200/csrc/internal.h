@@ -22,6 +22,9 @@ enum : unsigned int {
   ERR_SITE_TOPK = 0x20,
   ERR_SITE_ATTN = 0x30,
   ERR_SITE_COMBINE = 0x40,
+  ERR_SITE_NORM = 0x50,
+  ERR_SITE_CACHE = 0x60,
+  ERR_SITE_ATTN8 = 0x70,
 };
 
 #ifdef __CUDACC__
@@ -144,6 +147,21 @@ struct AttnArgs {
   bool decode;         // decode mode: the split-k memory-bound kernel where it applies
 };
 
+// attention over an 8-bit cache (attn8.cu)
+struct Attn8Args {
+  KvMap map;
+  const uint16_t* q;
+  const uint8_t* kv8;
+  const float* kv_scale;
+  const int32_t* idx;  // null: dense causal attention over every visible key
+  int dense_rows;      // query rows t < dense_rows take all visible keys (idx not read)
+  uint16_t* out;
+  float* lse;
+  void* ws;            // attn8_workspace_bytes, or null where it is 0
+  int B, T, S, H, d_k, d_v, k;
+  float tau;
+};
+
 // counts every kernel launch (dsa_launch_count)
 void note_launches(int n);
 
@@ -206,6 +224,10 @@ cudaError_t launch_indexer_bwd_tc(const LaunchCtx& c, const KvMap& map, const ui
                                   const float* w, const uint8_t* k_I, const float* k_scale, const float* grad,
                                   long long ld, const int32_t* idx, int B, int T, int k, int H_I, int q_begin,
                                   int q_count, float* dq, float* dw, float* dk);
+
+cudaError_t launch_attn8(const LaunchCtx& c, const Attn8Args& a);
+// scratch of launch_attn8 for the shape in `a` (pointers not read), sparse or dense
+size_t attn8_workspace_bytes(const Attn8Args& a, int num_sms);
 
 cudaError_t launch_wait_timeout_probe(const LaunchCtx& c);
 

@@ -31,6 +31,8 @@ EXPORTS = [
     "dsa_set_wait_timeout_us", "dsa_launch_count", "dsa_selftest_wait_timeout", "dsa_topk_static",
     "dsa_dense_attn", "dsa_topk_candidates", "dsa_topk_merge", "dsa_attn_combine", "dsa_select",
     "dsa_kl_target", "dsa_indexer_kl", "dsa_indexer_backward",
+    "dsa_norm_rope", "dsa_norm_rope_workspace_size", "dsa_norm_rope_backward", "dsa_cache_write", "dsa_cache_read",
+    "dsa_workspace8_size", "dsa_sparse_attn8", "dsa_dense_attn8", "dsa_forward8",
 ]
 
 
@@ -55,6 +57,20 @@ INPUT_NAMES = ("q_I", "q_scale", "w", "k_I", "k_scale", "q", "kv", "v")
 
 class Inputs(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in INPUT_NAMES]
+
+
+class NormRope(ctypes.Structure):
+    """dsa_norm_rope_desc; built by make_norm_rope."""
+    _fields_ = [("Hq", ctypes.c_int), ("Hk", ctypes.c_int), ("D", ctypes.c_int), ("norm_cols", ctypes.c_int),
+                ("rope_cols", ctypes.c_int), ("interleaved", ctypes.c_int), ("eps", ctypes.c_float),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p)]
+
+
+INPUT8_NAMES = ("q_I", "q_scale", "w", "k_I", "k_scale", "q", "kv8", "kv_scale")
+
+
+class Inputs8(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in INPUT8_NAMES]
 
 
 _lib = None
@@ -103,6 +119,25 @@ def lib() -> ctypes.CDLL:
         for fn in ("dsa_forward", "dsa_prefill", "dsa_decode"):
             getattr(L, fn).restype = i
             getattr(L, fn).argtypes = [sp, ctypes.POINTER(Inputs), vp, vp, vp, vp, sz, vp]
+        np_ = ctypes.POINTER(NormRope)
+        L.dsa_norm_rope.restype = i
+        L.dsa_norm_rope.argtypes = [sp, np_, vp, vp, vp, vp, vp]
+        L.dsa_norm_rope_workspace_size.restype = sz
+        L.dsa_norm_rope_workspace_size.argtypes = [sp, np_]
+        L.dsa_norm_rope_backward.restype = i
+        L.dsa_norm_rope_backward.argtypes = [sp, np_] + [vp] * 9 + [sz, vp]
+        L.dsa_cache_write.restype = i
+        L.dsa_cache_write.argtypes = [sp] + [vp] * 10
+        L.dsa_cache_read.restype = i
+        L.dsa_cache_read.argtypes = [sp, i, i] + [vp] * 7
+        L.dsa_workspace8_size.restype = sz
+        L.dsa_workspace8_size.argtypes = [sp]
+        L.dsa_sparse_attn8.restype = i
+        L.dsa_sparse_attn8.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.dsa_dense_attn8.restype = i
+        L.dsa_dense_attn8.argtypes = [sp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.dsa_forward8.restype = i
+        L.dsa_forward8.argtypes = [sp, ctypes.POINTER(Inputs8), vp, vp, vp, vp, sz, vp]
         L.dsa_get_device_error.restype = i
         L.dsa_get_device_error.argtypes = [vp, ctypes.POINTER(ctypes.c_int)]
         L.dsa_launch_count.restype = ctypes.c_ulonglong
@@ -366,6 +401,170 @@ def forward(shape: Shape, inp: dict, out, lse, idx, ws, entry: str = "dsa_forwar
         _need(lse, torch.float32, "lse")
     _check(entry, getattr(lib(), entry)(
         ctypes.byref(shape), ctypes.byref(ins), _p(out), _p(lse), _p(idx), _p(ws), ws.numel(), _stream()))
+    return out, lse, idx
+
+
+def _need_here(t, dtype, name, numel=None):
+    """As _need, on the current device, with exactly numel elements where that is given."""
+    if (t.dtype != dtype or not t.is_contiguous() or t.get_device() < 0
+            or t.get_device() != torch.cuda.current_device()):
+        raise ValueError(f"{name}: need a contiguous tensor of {dtype} on the current CUDA device, got {t.dtype} "
+                         f"on {t.device} contiguous={t.is_contiguous()}")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name}: need {numel} elements, got {t.numel()} ({tuple(t.shape)})")
+
+
+def _pool_rows(shape: Shape) -> int:
+    return shape.num_pages * shape.page_size if shape.page_size > 0 else shape.B * shape.S
+
+
+def make_norm_rope(*, Hq: int, Hk: int, D: int, norm_cols: int, rope_cols: int, interleaved: bool = False,
+                   eps: float = 1e-6, q_weight=None, k_weight=None, inv_freq=None) -> NormRope:
+    """Description of dsa_norm_rope's rows.  q_weight, k_weight: float32 CUDA
+    tensors [norm_cols] or None (ones); inv_freq: float32 CUDA tensor
+    [rope_cols / 2], radians per position.  It keeps references to them."""
+    for t, n, name in ((q_weight, norm_cols, "q_weight"), (k_weight, norm_cols, "k_weight"),
+                       (inv_freq, rope_cols // 2, "inv_freq")):
+        if t is not None:
+            _need_here(t, torch.float32, name, n)
+    d = NormRope(Hq, Hk, D, norm_cols, rope_cols, int(bool(interleaved)), eps,
+                 *(None if t is None else t.data_ptr() for t in (q_weight, k_weight, inv_freq)))
+    d._keep = (q_weight, k_weight, inv_freq)
+    return d
+
+
+def norm_rope(shape: Shape, desc: NormRope, q, k, q_out, k_out):
+    """RMS norm per head and rotation by position: q [B, T, Hq, D], k [B, T, Hk, D]
+    bf16 -> q_out, k_out (a side with no heads is None; in place is allowed)."""
+    n = shape.B * shape.T * desc.D
+    for t, H, name in ((q, desc.Hq, "q"), (q_out, desc.Hq, "q_out"), (k, desc.Hk, "k"), (k_out, desc.Hk, "k_out")):
+        if t is not None:
+            _need_here(t, torch.bfloat16, name, n * H)
+    _check("dsa_norm_rope", lib().dsa_norm_rope(
+        ctypes.byref(shape), ctypes.byref(desc), _p(q), _p(k), _p(q_out), _p(k_out), _stream()))
+    return q_out, k_out
+
+
+def norm_rope_workspace_size(shape: Shape, desc: NormRope) -> int:
+    return int(lib().dsa_norm_rope_workspace_size(ctypes.byref(shape), ctypes.byref(desc)))
+
+
+def alloc_norm_rope_workspace(shape: Shape, desc: NormRope) -> torch.Tensor:
+    n = norm_rope_workspace_size(shape, desc)
+    if n == 0:
+        raise DsaError("dsa_norm_rope_workspace_size", 1)
+    return torch.empty(n, dtype=torch.uint8, device="cuda")
+
+
+def norm_rope_backward(shape: Shape, desc: NormRope, q, k, dq_out, dk_out, dq, dk, dq_weight=None, dk_weight=None,
+                       ws=None):
+    """Gradients of norm_rope from its inputs and the gradients of its outputs;
+    dq_weight, dk_weight float32 [norm_cols] are written (None: not wanted)."""
+    n = shape.B * shape.T * desc.D
+    for t, H, name in ((q, desc.Hq, "q"), (dq_out, desc.Hq, "dq_out"), (dq, desc.Hq, "dq"),
+                       (k, desc.Hk, "k"), (dk_out, desc.Hk, "dk_out"), (dk, desc.Hk, "dk")):
+        if t is not None:
+            _need_here(t, torch.bfloat16, name, n * H)
+    for t, name in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
+        if t is not None:
+            _need_here(t, torch.float32, name, desc.norm_cols)
+    _check("dsa_norm_rope_backward", lib().dsa_norm_rope_backward(
+        ctypes.byref(shape), ctypes.byref(desc), _p(q), _p(k), _p(dq_out), _p(dk_out), _p(dq), _p(dk),
+        _p(dq_weight), _p(dk_weight), _p(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream()))
+    return dq, dk
+
+
+def cache_write(shape: Shape, *, kv=None, kv8=None, kv_scale=None, k_I=None, kI8=None, kI_scale=None,
+                q_I=None, qI8=None, qI_scale=None) -> None:
+    """Quantise a step's new rows to e4m3 and write them to their places: kv
+    [B, T, d_k] into the cache kv8, kv_scale; k_I [B, T, D_I] into kI8, kI_scale;
+    q_I [B, T, H_I, D_I] into qI8, qI_scale.  Each part may be left out."""
+    n, rows = shape.B * shape.T, _pool_rows(shape)
+    for x, x8, sc, d, m, r, name in ((kv, kv8, kv_scale, shape.d_k, n, rows, "kv"),
+                                     (k_I, kI8, kI_scale, shape.D_I, n, rows, "k_I"),
+                                     (q_I, qI8, qI_scale, shape.D_I, n * shape.H_I, n * shape.H_I, "q_I")):
+        if x is not None:
+            _need_here(x, torch.bfloat16, name, m * d)
+        if x8 is not None:
+            _need_here(x8, torch.uint8, name + " bytes", r * d)
+        if sc is not None:
+            _need_here(sc, torch.float32, name + " scales", r)
+    _check("dsa_cache_write", lib().dsa_cache_write(
+        ctypes.byref(shape), _p(kv), _p(kv8), _p(kv_scale), _p(k_I), _p(kI8), _p(kI_scale), _p(q_I), _p(qI8),
+        _p(qI_scale), _stream()))
+
+
+def cache_read(shape: Shape, s_begin: int, s_count: int, *, kv8=None, kv_scale=None, kv=None, kI8=None,
+               kI_scale=None, k_I=None) -> None:
+    """Tokens [s_begin, s_begin + s_count) of every sequence back as bf16 rows:
+    kv [B, s_count, d_k], k_I [B, s_count, D_I].  Each part may be left out."""
+    n, rows = shape.B * s_count, _pool_rows(shape)
+    for x, x8, sc, d, name in ((kv, kv8, kv_scale, shape.d_k, "kv"), (k_I, kI8, kI_scale, shape.D_I, "k_I")):
+        if x is not None:
+            _need_here(x, torch.bfloat16, name, n * d)
+        if x8 is not None:
+            _need_here(x8, torch.uint8, name + " bytes", rows * d)
+        if sc is not None:
+            _need_here(sc, torch.float32, name + " scales", rows)
+    _check("dsa_cache_read", lib().dsa_cache_read(
+        ctypes.byref(shape), s_begin, s_count, _p(kv8), _p(kv_scale), _p(kv), _p(kI8), _p(kI_scale), _p(k_I),
+        _stream()))
+
+
+def workspace8_size(shape: Shape) -> int:
+    return int(lib().dsa_workspace8_size(ctypes.byref(shape)))
+
+
+def alloc_workspace8(shape: Shape) -> torch.Tensor:
+    """dsa_workspace8_size bytes (sparse_attn8, dense_attn8, forward8)."""
+    n = workspace8_size(shape)
+    if n == 0:
+        raise DsaError("dsa_workspace8_size", 1)
+    return torch.empty(n, dtype=torch.uint8, device="cuda")
+
+
+def _need_attn8(shape, q, kv8, kv_scale, out, lse):
+    n, rows = shape.B * shape.T * shape.H, _pool_rows(shape)
+    _need_here(q, torch.bfloat16, "q", n * shape.d_k)
+    _need_here(kv8, torch.uint8, "kv8", rows * shape.d_k)
+    _need_here(kv_scale, torch.float32, "kv_scale", rows)
+    _need_here(out, torch.bfloat16, "out", n * shape.d_v)
+    if lse is not None:
+        _need_here(lse, torch.float32, "lse", n)
+
+
+def sparse_attn8(shape: Shape, q, kv8, kv_scale, idx, out, lse=None, ws=None):
+    """Step C over an 8-bit cache (e4m3 rows kv8, float32 scales kv_scale)."""
+    _need_attn8(shape, q, kv8, kv_scale, out, lse)
+    _need_here(idx, torch.int32, "idx", shape.B * shape.T * shape.k)
+    _check("dsa_sparse_attn8", lib().dsa_sparse_attn8(
+        ctypes.byref(shape), _p(q), _p(kv8), _p(kv_scale), _p(idx), _p(out), _p(lse), _p(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream()))
+    return out, lse
+
+
+def dense_attn8(shape: Shape, q, kv8, kv_scale, out, lse=None, ws=None):
+    """Dense causal attention over an 8-bit cache (no selection)."""
+    _need_attn8(shape, q, kv8, kv_scale, out, lse)
+    _check("dsa_dense_attn8", lib().dsa_dense_attn8(
+        ctypes.byref(shape), _p(q), _p(kv8), _p(kv_scale), _p(out), _p(lse), _p(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream()))
+    return out, lse
+
+
+def forward8(shape: Shape, inp: dict, out, lse, idx, ws):
+    """The whole path over an 8-bit cache through dsa_forward8."""
+    n, rows = shape.B * shape.T, _pool_rows(shape)
+    for t, d, m in (("q_I", torch.uint8, n * shape.H_I * shape.D_I), ("q_scale", torch.float32, n * shape.H_I),
+                    ("w", torch.float32, n * shape.H_I), ("k_I", torch.uint8, rows * shape.D_I),
+                    ("k_scale", torch.float32, rows)):
+        _need_here(inp[t], d, t, m)
+    _need_attn8(shape, inp["q"], inp["kv8"], inp["kv_scale"], out, lse)
+    _need_here(idx, torch.int32, "idx", n * shape.k)
+    ins = Inputs8(*(inp[t].data_ptr() for t in INPUT8_NAMES))
+    _check("dsa_forward8", lib().dsa_forward8(
+        ctypes.byref(shape), ctypes.byref(ins), _p(out), _p(lse), _p(idx), _p(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream()))
     return out, lse, idx
 
 
