@@ -18,26 +18,36 @@
 //     BF16 number has 8 significant bits and e4m3 four, so the two terms give
 //     q exactly down to 2^-10 of the row's largest, and within 2^-19 of it
 //     below (e4m3's subnormal step);
-//   * P = P_hi + P_lo, rounded to nearest at 2^-9 of P or better (BF16 would
-//     be 2^-9).  R is kept so that the largest P of a row lies in [2^6, 2^8]:
-//     the subnormal step is then 2^-15 of the largest or less.
+//   * P = P_hi + P_lo, rounded to nearest at 2^-8 of P at worst and 2^-10.6
+//     in the mean square (one BF16 number: 2^-9 and 2^-9.3).  R is kept so
+//     that the largest P of a row is at least 2^4: e4m3's subnormal half step
+//     is then 2^-14 of it or less.
 // Logits, P before its rounding, l and the output accumulate in FP32.
 //
-// Work split.  All heads of one query are the MMA M dimension (128 rows).
-// A 128 x 512 FP32 accumulator would fill TMEM, so two CTAs share a query,
-// one per half of the value columns; few queries also split their keys, and
-// a combine kernel merges the parts.
-// Per CTA: TMEM holds O (128 x 256) | two S/P buffers of 64 columns | q_hi
-// and q_lo of the first 256 key columns.  Shared memory holds the rest of q
-// (80 KB) and a ring of four slots of 64 keys (144 KB).
-// Warp roles (384 threads): warp 0 issues the MMAs; warp 1 forms the
-// per-key constants; warps 2 and 3 gather rows with 16-byte cp.async
-// that arrive on the slot's barrier by themselves; warps 4-7 and 8-11 are two
-// softmax groups that take the chunks in turn (thread = head row), so a
-// group has two chunk periods for its work.  The reference R goes from one
-// group to the other through shared memory; it moves only when a chunk's
-// maximum exceeds it by 2 (log2 units), and then the accumulator is rescaled
-// once, after the P V before it.
+// Work split.  A CTA takes 64 heads of one query (all of them when there are
+// no more) and all value columns, as the M = 64 of tcgen05.mma.ws: that form
+// spreads a 64 x N result over all 128 TMEM lanes (lanes 0-63 the first N/2
+// columns, 64-127 the rest), so the 64 x 512 FP32 accumulator takes half of
+// TMEM.  With M = 128 it would fill TMEM, and the way out, a CTA per half of
+// the value columns, computes every logit twice.  Measured, back to back:
+// N = 128 45-49 cycles, N = 256 77-82 (M = 128: 64 and 129), so a query's
+// 128 keys cost 2 x 3000 cycles in place of 2 x 4400 (M = 128 with the N = 64
+// that fits beside the accumulator).  Few queries also split their keys, and a
+// combine kernel merges the parts.
+//
+// Per CTA: TMEM holds O (256 columns) | two S buffers of 64 | q_hi and q_lo of
+// the first 256 key columns, in both lane halves.  Shared memory holds the
+// rest of q (40 KB), two regions of 128 keys (144 KB) and two P buffers.
+// Chunks a, b of 128 keys alternate between the regions, and the tensor core
+// gets q K^T(a), q K^T(b), P V(a), P V(b): the softmax of a runs under
+// q K^T(b), that of b under P V(a), and the next a is gathered under P V(b),
+// the next b under q K^T.
+// Warp roles (576 threads): warp 0 issues the MMAs; warp 1 forms the per-key
+// constants; warps 2-9 are the softmax, warps 10-17 gather 16 keys each with
+// 16-byte cp.async that arrive on the region's barrier by themselves.  Four
+// softmax threads share a head row (32 keys each) and exchange their maxima
+// through shared memory.  R moves only when a chunk's maximum exceeds it by
+// kSlack, and then the accumulator is rescaled once.
 #include <cuda_fp8.h>
 #include <math.h>
 
@@ -49,44 +59,46 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kN = 64;                 // keys per chunk
-constexpr int kSlots = 4;              // chunks the ring holds
-constexpr int kRing = kN * kSlots;     // ring rows
-constexpr int kMmaWarp = 0, kParamWarp = 1, kFirstSoftmax = 4;
-constexpr int kThreads = 384;         // 12 warps: 168 registers a thread
+constexpr int kN = 128;                // keys per chunk
+constexpr int kM = 64;                 // heads per CTA
+constexpr int kMmaWarp = 0, kParamWarp = 1, kFirstSoftmax = 2, kFirstGather = 10, kGatherWarps = 8;
+constexpr int kThreads = 32 * (kFirstGather + kGatherWarps);
 constexpr uint32_t kTmemCols = 512;
-constexpr float kHead = 6.f;           // log2 of the largest P of a row when R is set
-constexpr float kSlack = 2.f;          // how far a maximum may pass before R moves (2^(6+2) < 448)
+constexpr float kHead = 4.f;           // log2 of the largest P of a row when R is set
+constexpr float kSlack = 4.75f;        // how far a maximum may pass before R moves (2^(4 + 4.75) < 448)
 
 template <int DK, int DV>
 struct Cfg {
   static constexpr int KSTEPS = (DK + 31) / 32;        // 32-byte MMA K steps
   static constexpr int NF = DK >= 128 ? DK / 128 : 1;  // 128-byte atoms of a row
   static constexpr int TAIL = DK > NF * 128 ? 1 : 0;   // one 64-byte atom more
-  static constexpr int NHALF = DV >= 128 ? 2 : 1;
-  static constexpr int DVH = DV / NHALF;
+  static constexpr int NV = DV < 256 ? DV : 256;       // value columns of one MMA
+  static constexpr int NMMV = DV / NV;
+  static constexpr int OCOLS = DV / 2;                 // TMEM columns of the accumulator
   static constexpr uint32_t OCOL = 0;
-  static constexpr uint32_t SCOL = DVH;
-  static constexpr uint32_t QCOL = SCOL + 2 * kN;
-  // leading key columns whose q lies in TMEM (whole atoms)
-  static constexpr int QT = (int)(kTmemCols - QCOL) / 2 * 4 / 128 * 128 >= DK ? 0 : (int)(kTmemCols - QCOL) / 2 * 4 / 128 * 128;
+  static constexpr uint32_t SCOL = 256;
+  static constexpr uint32_t QCOL = SCOL + 2 * (kN / 2);
+  static constexpr int QT = DK > 256 ? 256 : 0;        // leading key columns whose q lies in TMEM
   static constexpr int QSF = NF - QT / 128;            // q atoms in shared memory
-  static constexpr int QPIECE = QSF * 128 * 128 + TAIL * 128 * 64;
-  static constexpr int ATOM = kRing * 128;             // bytes of one ring atom
-  static constexpr int RING_BYTES = NF * ATOM + TAIL * kRing * 64;
+  static constexpr int QPIECE = QSF * kM * 128 + TAIL * kM * 64;
+  static constexpr int ATOM = 2 * kN * 128;            // bytes of one atom of both regions
+  static constexpr int KV_BYTES = NF * ATOM + TAIL * 2 * kN * 64;
+  static constexpr int PTERM = kM * kN;                // bytes of one term of a P buffer
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_KV = 2 * QPIECE;
-  static constexpr int OFF_PAR = OFF_KV + RING_BYTES;  // [2][64] {a s, log2 s}, [2][64] 1 / s
-  static constexpr int OFF_M = OFF_PAR + 2 * kN * 12;  // [128] the running reference
-  static constexpr int OFF_BAR = OFF_M + 128 * 4;
-  static constexpr int NBARS = 1 + 2 * kSlots + 2 + 2 + 2 + 2 + 1 + 8;
+  static constexpr int OFF_KV = (2 * QPIECE + 1023) / 1024 * 1024;
+  static constexpr int OFF_P = OFF_KV + KV_BYTES;      // [2][hi, lo][64 rows x 128 bytes]
+  static constexpr int OFF_PAR = OFF_P + 4 * PTERM;    // [2][128] {a s, log2 s}, [2][128] 1 / s
+  static constexpr int OFF_MX = OFF_PAR + 2 * kN * 12; // [2][4][64] partial maxima
+  static constexpr int OFF_E = OFF_MX + 2 * 4 * kM * 4;  // [64] 2^e of the head rows
+  static constexpr int OFF_BAR = OFF_E + kM * 4;
+  static constexpr int NBARS = 1 + 2 + 4 + 2 + 2 + 2 + 2 + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;
   static constexpr int BYTES = OFF_MISC + 16;
   static_assert(BYTES <= 232448, "shared memory per CTA");
-  static_assert(OFF_KV % 1024 == 0 && OFF_BAR % 8 == 0, "alignment");
-  static_assert(QCOL + 2 * (QT / 4) <= kTmemCols, "TMEM");
-  // q's bytes on their way to TMEM pass through the ring's upper half
-  static_assert(QT == 0 || (2 * QT * 128 <= 2 * 128 * 128 * 2), "staging");
+  static_assert(OFF_KV % 1024 == 0 && OFF_P % 1024 == 0 && OFF_BAR % 8 == 0, "alignment");
+  static_assert(OCOLS <= 256 && QCOL + 2 * (QT / 4) <= kTmemCols, "TMEM");
+  // q's bytes on their way to TMEM pass through the P buffers
+  static_assert(2 * QT * kM <= 4 * PTERM, "staging");
 };
 
 struct Params {
@@ -101,7 +113,7 @@ struct Params {
   float* part_o;         // [rows, nsplit, H, d_v] (nsplit > 1), normalised by the part's own l
   float* part_lse;       // [rows, nsplit, H], log2 units
   int T, H, k;
-  int rows, nsplit;
+  int rows, nsplit, hsplit;
   float scale_log2;      // tau log2(e)
   long long wait_ns;
   DevErr* err;
@@ -110,7 +122,7 @@ struct Params {
 __device__ __forceinline__ int pow2_exponent(float amax) {
   const uint32_t u = __float_as_uint(amax);
   const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return max(e, -100);
+  return min(max(e, -100), 120);
 }
 __device__ __forceinline__ uint32_t e4m3x2_of_half2(__half2 h) {
   return (uint32_t)__nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<__half2_raw*>(&h), __NV_SATFINITE, __NV_E4M3);
@@ -125,16 +137,48 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   lo = e4m3x2_of_half2(__hsub2(h, half2_of_e4m3x2(hi)));
 }
 
-__device__ __forceinline__ void mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+// D[tmem] (+)= A B^T, e4m3, the M = 64 form that uses all lanes; A in shared
+// memory or in TMEM (in lanes 0-63 and again in 64-127)
+__device__ __forceinline__ void mma_ws(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.ws.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ws_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "tcgen05.mma.ws.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// W columns of TMEM times alpha (32 lanes of one warp)
+template <int W>
+__device__ __forceinline__ void tmem_scale(uint32_t addr, float alpha) {
+  if constexpr (W == 32) {
+    uint32_t o[32];
+    tmem_ld32(addr, o);
+    tmem_wait_ld_dep(o);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+    tmem_st32(addr, o);
+  } else {
+    uint32_t o[16];
+    tmem_ld16(addr, o);
+    tmem_wait_ld_dep(o);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+    tmem_st16(addr, o);
+  }
+}
 
 template <int DK, int DV, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
@@ -147,25 +191,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
   }
   uint8_t* sQ = smem + C::OFF_Q;
   uint8_t* sKV = smem + C::OFF_KV;
-  float2* sPar = reinterpret_cast<float2*>(smem + C::OFF_PAR);        // [2][64]
+  uint8_t* sP = smem + C::OFF_P;
+  float2* sPar = reinterpret_cast<float2*>(smem + C::OFF_PAR);        // [2][128]
   float* sInv = reinterpret_cast<float*>(smem + C::OFF_PAR + 2 * kN * 8);
-  float* sM = reinterpret_cast<float*>(smem + C::OFF_M);
+  float* sMx = reinterpret_cast<float*>(smem + C::OFF_MX);
+  float* sE = reinterpret_cast<float*>(smem + C::OFF_E);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* q_ready = bars;                    // q in shared memory and TMEM (8 softmax warps)
-  uint64_t* kv_full = q_ready + 1;             // [slot] rows landed (2 gather warps, every lane)
-  uint64_t* kv_empty = kv_full + kSlots;       // [slot] P V of the slot's chunk complete (commit)
-  uint64_t* par_full = kv_empty + kSlots;      // [2] per-key constants written (32 lanes)
-  uint64_t* par_empty = par_full + 2;          // [2] and read (4 warps)
-  uint64_t* s_full = par_empty + 2;            // [2] Q K^T complete (commit)
-  uint64_t* p_full = s_full + 2;               // [2] P written (4 warps)
+  uint64_t* kv_full = q_ready + 1;             // [region] rows landed (8 gather warps, every lane)
+  uint64_t* kv_empty = kv_full + 2;            // [region][half] P V of the half's keys complete (commit)
+  uint64_t* par_full = kv_empty + 4;           // [2] per-key constants written (32 lanes)
+  uint64_t* par_empty = par_full + 2;          // [2] and read (8 warps)
+  uint64_t* s_full = par_empty + 2;            // [2] q K^T complete (commit)
+  uint64_t* p_full = s_full + 2;               // [2] P written (8 warps)
   uint64_t* mma_done = p_full + 2;
-  uint64_t* m_bar = mma_done + 1;              // [2 groups][4 quarters] reference published
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int half = blockIdx.x % C::NHALF;
-  const int rest = blockIdx.x / C::NHALF;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int hs = blockIdx.x % p.hsplit;        // heads [64 hs, 64 hs + 64)
+  const int rest = blockIdx.x / p.hsplit;
   const int row = rest / p.nsplit;             // b * T + t
   const int split = rest - row * p.nsplit;
   const int b = row / p.T, t = row - b * p.T;
@@ -179,18 +224,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
 
   if (threadIdx.x == 0) {
     mbar_init(q_ready, 8);
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&kv_full[i], 64);
-      mbar_init(&kv_empty[i], 1);
-    }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&kv_full[i], 32 * kGatherWarps);
+      mbar_init(&kv_empty[2 * i], 1);
+      mbar_init(&kv_empty[2 * i + 1], 1);
       mbar_init(&par_full[i], 32);
-      mbar_init(&par_empty[i], 4);
+      mbar_init(&par_empty[i], 8);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], 8);
     }
     mbar_init(mma_done, 1);
-    for (int i = 0; i < 8; ++i) mbar_init(&m_bar[i], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -199,16 +242,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     tmem_relinquish();
   }
   if constexpr (DK % 128 != 0 && C::TAIL == 0) {
-    // columns DK.. of the ring's atom meet zero columns of q in the last K
+    // columns DK.. of the keys' atom meet zero columns of q in the last K
     // step: they must not hold NaN bytes
-    for (int i = threadIdx.x; i < kRing * 8; i += kThreads)
-      if (i % 8 >= DK / 16) *reinterpret_cast<uint4*>(sKV + (i / 8) * 128 + (((i % 8) ^ ((i / 8) & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = threadIdx.x; i < 2 * kN * 8; i += kThreads)
+      if (i % 8 >= DK / 16)
+        *reinterpret_cast<uint4*>(sKV + (i / 8) * 128 + (((i % 8) ^ ((i / 8) & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   const AbortSources ab{abort_flag, &p.err->code};
   const AbortSources no_abort{nullptr, nullptr};
@@ -221,37 +265,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     return __all_sync(0xffffffffu, r);
   };
   const int32_t* irow = dense ? nullptr : p.idx + (size_t)row * p.k;
-  // index of slot s of this split; -1 past the end, for an empty slot and for
-  // an index outside [0, L_b)
+  // index of slot s of this split; -1 past the end and for an empty slot
   auto load_idx = [&](int s) -> int { return s < slot1 ? (dense ? s : irow[s]) : -1; };
-  // cache row (relative to the sequence's first in a contiguous cache) or -1
+  // cache row (relative to the sequence's first in a contiguous cache); -1
+  // for no key and for an index outside [0, L_b)
   auto row_of = [&](int v) -> int {
     if (v < 0 || v >= Lb) return -1;
     return PAGED ? (int)p.map.row<true>(b, v) : v;
   };
   const long long base_row = PAGED ? 0 : (long long)b * p.map.S;
 
-  if (warp == 2 || warp == 3) {
+  if (warp >= kFirstGather) {
     // ------------------------------------------------------------ gather
-    // warp g copies keys [32 g, 32 g + 32) of every chunk
-    const int g = warp - 2;
+    // warp g copies keys [16 g, 16 g + 16) of every chunk
+    const int g = warp - kFirstGather;
     const uint8_t* base = p.kv8 + base_row * DK;
-    const int kl = 32 * g + lane;
+    const int kl = 16 * g + (lane & 15);
     int r_cur = row_of(load_idx(slot0 + kl));
     int i_next = load_idx(slot0 + kN + kl);
-    bool ok = true;
     for (int j = 0; j < nchunks; ++j) {
-      const int st = j % kSlots;
-      if (j >= kSlots && !wwait(&kv_empty[st], (uint32_t)(j / kSlots - 1) & 1)) { fail(1); ok = false; break; }
-      // q's bytes pass through slots 2 and 3 on their way to TMEM
-      if (C::QT > 0 && (j == 2 || j == 3) && !wwait(q_ready, 0)) { fail(2); ok = false; break; }
+      const int rg = j & 1;
+      if (j >= 2 && !wwait(&kv_empty[2 * rg + g / 4], (uint32_t)(j / 2 - 1) & 1)) { fail(1); break; }
       const int r_next = row_of(i_next);
       i_next = load_idx(slot0 + (j + 2) * kN + kl);
-      uint8_t* dst0 = sKV + (st * kN + 32 * g) * 128;
-      const int c = lane & 7, rg = lane >> 3;
+      uint8_t* dst0 = sKV + (rg * kN + 16 * g) * 128;
+      const int c = lane & 7, k8 = lane >> 3;
 #pragma unroll
-      for (int m = 0; m < 8; ++m) {
-        const int kr = 4 * m + rg;                       // key within the warp's 32
+      for (int m = 0; m < 4; ++m) {
+        const int kr = 4 * m + k8;                       // key within the warp's 16
         const int r = __shfl_sync(0xffffffffu, r_cur, kr);
         const uint8_t* src = base + (size_t)(r < 0 ? 0 : r) * DK + c * 16;
         uint8_t* dst = dst0 + kr * 128 + ((c ^ (kr & 7)) << 4);
@@ -260,53 +301,54 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
           if (a * 128 + c * 16 < DK) cp_async16_zfill(dst + a * C::ATOM, src + a * 128, r < 0 ? 0u : 16u);
       }
       if constexpr (C::TAIL != 0) {
-        const int c4 = lane & 3, rg8 = lane >> 2;
-        uint8_t* tail0 = sKV + C::NF * C::ATOM + (st * kN + 32 * g) * 64;
+        const int c4 = lane & 3, k4 = lane >> 2;
+        uint8_t* tail0 = sKV + C::NF * C::ATOM + (rg * kN + 16 * g) * 64;
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const int kr = 8 * m + rg8;
+        for (int m = 0; m < 2; ++m) {
+          const int kr = 8 * m + k4;
           const int r = __shfl_sync(0xffffffffu, r_cur, kr);
           cp_async16_zfill(tail0 + kr * 64 + ((c4 ^ ((kr >> 1) & 3)) << 4),
                            base + (size_t)(r < 0 ? 0 : r) * DK + C::NF * 128 + c4 * 16, r < 0 ? 0u : 16u);
         }
       }
-      cp_async_arrive(&kv_full[st]);
+      cp_async_arrive(&kv_full[rg]);
       r_cur = r_next;
     }
-    (void)ok;
     cp_async_commit();
     cp_async_wait<0>();
   } else if (warp == kParamWarp) {
     // ------------------------------------------------------------ per-key constants
-    // lane l holds keys l and l + 32 of a chunk
+    // lane l holds keys l, l + 32, l + 64, l + 96 of a chunk
     auto scale_of = [&](int r) -> float { return r < 0 ? 0.f : __ldg(p.kv_scale + base_row + r); };
     auto checked_row = [&](int v) -> int {
       if (v >= Lb) {
-        if (half == 0) report_error(p.err, DSA_ERR_DEVICE_BOUNDS, ERR_SITE_ATTN8);
+        if (hs == 0) report_error(p.err, DSA_ERR_DEVICE_BOUNDS, ERR_SITE_ATTN8);
         return -1;
       }
       const int r = row_of(v);
-      if (PAGED && v >= 0 && r < 0 && half == 0) report_error(p.err, DSA_ERR_DEVICE_BOUNDS, ERR_SITE_ATTN8 | (1u << 8));
+      if (PAGED && v >= 0 && r < 0 && hs == 0) report_error(p.err, DSA_ERR_DEVICE_BOUNDS, ERR_SITE_ATTN8 | (1u << 8));
       return r;
     };
-    int i_next[2];
-    float s_cur[2];
+    int i_next[4];
+    float s_cur[4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      s_cur[u] = scale_of(checked_row(load_idx(slot0 + lane + 32 * u)));
+    for (int u = 0; u < 4; ++u) i_next[u] = load_idx(slot0 + lane + 32 * u);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      s_cur[u] = scale_of(checked_row(i_next[u]));
       i_next[u] = load_idx(slot0 + kN + lane + 32 * u);
     }
     for (int j = 0; j < nchunks; ++j) {
-      float s_next[2];
+      float s_next[4];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < 4; ++u) {
         s_next[u] = scale_of(checked_row(i_next[u]));
         i_next[u] = load_idx(slot0 + (j + 2) * kN + lane + 32 * u);
       }
       const int pb = j & 1;
       if (j >= 2 && !wwait(&par_empty[pb], (uint32_t)(j / 2 - 1) & 1)) { fail(3); break; }
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < 4; ++u) {
         const float s = s_cur[u];
         const bool on = s > 0.f;
         sPar[pb * kN + lane + 32 * u] = make_float2(p.scale_log2 * s, on ? log2f(s) : -INFINITY);
@@ -317,155 +359,185 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issue
-    if (lane == 0 && nchunks > 0) {
-      constexpr uint32_t idesc_qk = make_idesc(kFmtE4M3, kFmtE4M3, 0, 0, 128, kN);
-      constexpr uint32_t idesc_pv = make_idesc(kFmtE4M3, kFmtE4M3, 0, 1, 128, C::DVH);
+    // the whole warp runs this code and one elected lane issues, so that the
+    // descriptors stay in uniform registers: a lane alone on its branch took
+    // 80 cycles an MMA, more than the tensor core
+    if (nchunks > 0) {
+      constexpr uint32_t idesc_qk = make_idesc(kFmtE4M3, kFmtE4M3, 0, 0, kM, kN);
+      constexpr uint32_t idesc_pv = make_idesc(kFmtE4M3, kFmtE4M3, 0, 1, kM, C::NV);
       const uint64_t kdesc0 = make_sdesc(smem_u32(sKV), 16, 1024, kSwizzle128);
       const uint64_t ktail0 = make_sdesc(smem_u32(sKV) + C::NF * C::ATOM, 16, 512, kSwizzle64);
       const uint64_t qdesc0 = make_sdesc(smem_u32(sQ), 16, 1024, kSwizzle128);
-      const uint64_t qtail0 = make_sdesc(smem_u32(sQ) + C::QSF * 128 * 128, 16, 512, kSwizzle64);
-      const uint64_t vdesc0 = make_sdesc(smem_u32(sKV) + (uint32_t)(half * (C::DVH / 128)) * C::ATOM, C::ATOM, 1024,
-                                         kSwizzle128);
-      bool ok = mbar_wait(q_ready, 0, p.wait_ns, ab);
+      const uint64_t qtail0 = make_sdesc(smem_u32(sQ) + C::QSF * kM * 128, 16, 512, kSwizzle64);
+      const uint64_t vdesc0 = make_sdesc(smem_u32(sKV), C::ATOM, 1024, kSwizzle128);
+      const uint64_t pdesc0 = make_sdesc(smem_u32(sP), 16, 1024, kSwizzle128);
+      const bool leader = elect_one() != 0;
+      bool ok = wwait(q_ready, 0);
       if (!ok) fail(4);
-      tc_fence_after();
       int qk = 0, pv = 0;
-      // S(j) = q K^T: both terms of q over the key columns in steps of 32
-      auto issue_qk = [&]() -> bool {
-        const int st = qk % kSlots, sb = qk & 1;
-        if (!mbar_wait(&kv_full[st], (uint32_t)(qk / kSlots) & 1, p.wait_ns, ab)) { fail(5); return false; }
+      // S = q K^T of chunk qk: both terms of q over the key columns, in steps of 32
+      auto issue_qk = [&]() {
+        const int rg = qk & 1;
+        if (!wwait(&kv_full[rg], (uint32_t)(qk / 2) & 1)) { fail(5); ok = false; return; }
         fence_proxy_async_smem();
         tc_fence_after();
-        const uint64_t kst = kdesc0 + (uint64_t)((st * kN * 128) >> 4);
-        const uint64_t ktl = ktail0 + (uint64_t)((st * kN * 64) >> 4);
-        const uint32_t dS = tmem + C::SCOL + sb * kN;
+        if (leader) {
+          const uint64_t kst = kdesc0 + (uint64_t)((rg * kN * 128) >> 4);
+          const uint64_t ktl = ktail0 + (uint64_t)((rg * kN * 64) >> 4);
+          const uint32_t dS = tmem + C::SCOL + rg * (kN / 2);
 #pragma unroll
-        for (int term = 0; term < 2; ++term)
+          for (int ks = 0; ks < C::KSTEPS; ++ks)
 #pragma unroll
-          for (int ks = 0; ks < C::KSTEPS; ++ks) {
-            const int d = ks * 32;
-            const uint32_t acc = (term > 0 || ks > 0) ? 1u : 0u;
-            if (d < C::NF * 128) {
-              const uint64_t bdesc = kst + (uint64_t)(((d / 128) * C::ATOM + (d % 128)) >> 4);
-              if (d < C::QT) {
-                mma_f8_ts(dS, tmem + C::QCOL + term * (C::QT / 4) + d / 4, bdesc, idesc_qk, acc);
+            for (int term = 0; term < 2; ++term) {
+              const int d = ks * 32;
+              const uint32_t acc = (term > 0 || ks > 0) ? 1u : 0u;
+              if (d < C::NF * 128) {
+                const uint64_t bdesc = kst + (uint64_t)(((d / 128) * C::ATOM + (d % 128)) >> 4);
+                if (d < C::QT) {
+                  mma_ws_ts(dS, tmem + C::QCOL + term * (C::QT / 4) + d / 4, bdesc, idesc_qk, acc);
+                } else {
+                  const int dq = d - C::QT;
+                  mma_ws(dS, qdesc0 + (uint64_t)((term * C::QPIECE + (dq / 128) * (kM * 128) + (dq % 128)) >> 4), bdesc,
+                         idesc_qk, acc);
+                }
               } else {
-                const int dq = d - C::QT;
-                mma_f8(dS, qdesc0 + (uint64_t)((term * C::QPIECE + (dq / 128) * 16384 + (dq % 128)) >> 4), bdesc,
-                       idesc_qk, acc);
+                const int dt = d - C::NF * 128;
+                mma_ws(dS, qtail0 + (uint64_t)((term * C::QPIECE + dt) >> 4), ktl + (uint64_t)(dt >> 4), idesc_qk, acc);
               }
-            } else {
-              const int dt = d - C::NF * 128;
-              mma_f8(dS, qtail0 + (uint64_t)((term * C::QPIECE + dt) >> 4), ktl + (uint64_t)(dt >> 4), idesc_qk, acc);
             }
-          }
-        mma_commit(&s_full[sb]);
+          mma_commit(&s_full[rg]);
+        }
+        __syncwarp();
         ++qk;
-        return true;
       };
-      ok = ok && issue_qk();
-      while (ok && pv < nchunks) {
-        // Q K^T of the next chunk goes ahead of this chunk's P V, over the
-        // S/P buffer of the P V before it: the tensor core takes the MMAs of
-        // one thread in the order of their issue
-        if (qk < nchunks && !issue_qk()) { ok = false; break; }
-        const int st = pv % kSlots, sb = pv & 1;
-        if (!mbar_wait(&p_full[sb], (uint32_t)(pv / 2) & 1, p.wait_ns, ab)) { fail(6); ok = false; break; }
+      // O += P V of chunk pv; each half of the region is free once its keys are done
+      auto issue_pv = [&]() {
+        const int rg = pv & 1;
+        if (!wwait(&p_full[rg], (uint32_t)(pv / 2) & 1)) { fail(6); ok = false; return; }
         tc_fence_after();
-        const uint64_t vst = vdesc0 + (uint64_t)((st * kN * 128) >> 4);
+        if (leader) {
+          const uint64_t vst = vdesc0 + (uint64_t)((rg * kN * 128) >> 4);
+          const uint64_t pst = pdesc0 + (uint64_t)((rg * 2 * C::PTERM) >> 4);
 #pragma unroll
-        for (int ks = 0; ks < kN / 32; ++ks)
+          for (int ks = 0; ks < kN / 32; ++ks) {
 #pragma unroll
-          for (int term = 0; term < 2; ++term)
-            mma_f8_ts(tmem + C::OCOL, tmem + C::SCOL + sb * kN + term * (kN / 4) + ks * 8,
-                      vst + (uint64_t)((ks * 32 * 128) >> 4), idesc_pv, (pv > 0 || ks > 0 || term > 0) ? 1u : 0u);
-        mma_commit(&kv_empty[st]);
+            for (int nv = 0; nv < C::NMMV; ++nv)
+#pragma unroll
+              for (int term = 0; term < 2; ++term)
+                mma_ws(tmem + C::OCOL + nv * (C::NV / 2), pst + (uint64_t)((term * C::PTERM + ks * 32) >> 4),
+                       vst + (uint64_t)((nv * (C::NV / 128) * C::ATOM + ks * 32 * 128) >> 4), idesc_pv,
+                       (pv > 0 || ks > 0 || term > 0) ? 1u : 0u);
+            if (ks & 1) mma_commit(&kv_empty[2 * rg + ks / 2]);
+          }
+        }
+        __syncwarp();
         ++pv;
+      };
+      while (ok && pv < nchunks) {
+        issue_qk();
+        if (ok && qk < nchunks) issue_qk();
+        while (ok && pv < qk) issue_pv();
       }
-      mma_commit(mma_done);
-      mbar_wait(mma_done, 0, p.wait_ns, no_abort);
-      // drain: the last arrivals of the commit-fed barriers
-      for (int i = max(0, pv - kSlots); i < pv; ++i)
-        mbar_wait(&kv_empty[i % kSlots], (uint32_t)(i / kSlots) & 1, p.wait_ns, no_abort);
-      for (int i = max(0, qk - 2); i < qk; ++i) mbar_wait(&s_full[i & 1], (uint32_t)(i / 2) & 1, p.wait_ns, no_abort);
+      if (leader) {
+        mma_commit(mma_done);
+        mbar_wait(mma_done, 0, p.wait_ns, no_abort);
+        // drain: the last arrivals of the commit-fed barriers
+        for (int i = max(0, pv - 2); i < pv; ++i)
+          for (int u = 0; u < 2; ++u) mbar_wait(&kv_empty[2 * (i & 1) + u], (uint32_t)(i / 2) & 1, p.wait_ns, no_abort);
+        for (int i = max(0, qk - 2); i < qk; ++i) mbar_wait(&s_full[i & 1], (uint32_t)(i / 2) & 1, p.wait_ns, no_abort);
+      }
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ softmax + output
-    const int grp = (warp - kFirstSoftmax) >> 2, quarter = warp & 3;
-    const int h = quarter * 32 + lane;                   // head row == TMEM lane
+    // lane quarter `quarter` of TMEM: head rows 32 (quarter & 1) + lane, keys
+    // 64 (quarter / 2) of a chunk; of those, warp side `c` takes 32
+    const int sw = warp - kFirstSoftmax;                 // 0..7
+    const int quarter = warp & 3, c = sw >> 2;
+    const int r = (quarter & 1) * 32 + lane, kg = quarter >> 1;
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+    const int h = hs * kM + r;
     const bool head_ok = h < p.H;
-    uint8_t* stage = sKV + 2 * kN * 128;                 // ring slots 2 and 3 of each atom
     float f_h = 0.f;
     if (nchunks > 0) {
-      // q rows: a warp takes a row at a time, 16 rows; the row's exponent from
+      // q rows: a warp takes 8 rows, four in flight; the row's exponent from
       // its maximum, then the two terms of eight columns per lane and step
       constexpr int QV = (DK + 255) / 256;               // 8-column vectors per lane
-      const int sw = warp - kFirstSoftmax;
-      for (int i = 0; i < 16; ++i) {
-        const int hr = sw * 16 + i;
-        uint4 v[QV];
-        float amax = 0.f;
+      constexpr int QR = 4;
+#pragma unroll 1
+      for (int i0 = 0; i0 < 8; i0 += QR) {
+        uint4 v[QR][QV];
 #pragma unroll
-        for (int u = 0; u < QV; ++u) {
-          const int col = (u * 32 + lane) * 8;
-          v[u] = make_uint4(0u, 0u, 0u, 0u);
-          if (hr < p.H && col < DK) v[u] = *reinterpret_cast<const uint4*>(p.q + ((size_t)row * p.H + hr) * DK + col);
-          const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        for (int i = 0; i < QR; ++i)
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            amax = fmaxf(amax, fmaxf(__uint_as_float((w[x] & 0x7fffu) << 16), __uint_as_float(w[x] & 0x7fff0000u)));
-        }
+          for (int u = 0; u < QV; ++u) {
+            const int hr = hs * kM + sw * 8 + i0 + i, col = (u * 32 + lane) * 8;
+            v[i][u] = make_uint4(0u, 0u, 0u, 0u);
+            if (hr < p.H && col < DK)
+              v[i][u] = __ldg(reinterpret_cast<const uint4*>(p.q + ((size_t)row * p.H + hr) * DK + col));
+          }
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-        const int e = pow2_exponent(amax);
-        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-        if (lane == 0) sM[hr] = __uint_as_float((uint32_t)(127 + e) << 23);
+        for (int i = 0; i < QR; ++i) {
+          const int rr = sw * 8 + i0 + i;
+          float amax = 0.f;
 #pragma unroll
-        for (int u = 0; u < QV; ++u) {
-          const int col = (u * 32 + lane) * 8;
-          if (col >= C::NF * 128 + C::TAIL * 64) continue;   // columns DK.. of the last atom are written as zeros
-          const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-          uint32_t hi[4], lo[4];
+          for (int u = 0; u < QV; ++u) {
+            const uint32_t w[4] = {v[i][u].x, v[i][u].y, v[i][u].z, v[i][u].w};
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            split2(__uint_as_float(w[x] << 16) * inv, __uint_as_float(w[x] & 0xffff0000u) * inv, hi[x], lo[x]);
-          const uint2 H = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-          const uint2 L = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-          const int c16 = (col % 128) / 16, sub = col % 16;
-          if (col < C::QT) {
-            // staged [atom][128 rows x 128 bytes], hi in the ring's atoms 0, 1, lo in 2, 3
-            uint8_t* d = stage + (col / 128) * C::ATOM + hr * 128 + ((c16 ^ (hr & 7)) << 4) + sub;
-            *reinterpret_cast<uint2*>(d) = H;
-            *reinterpret_cast<uint2*>(d + (C::QT / 128) * C::ATOM) = L;
-          } else if (col < C::NF * 128) {
-            uint8_t* d = sQ + ((col - C::QT) / 128) * 16384 + hr * 128 + ((c16 ^ (hr & 7)) << 4) + sub;
-            *reinterpret_cast<uint2*>(d) = H;
-            *reinterpret_cast<uint2*>(d + C::QPIECE) = L;
-          } else {
-            const int ct = (col - C::NF * 128) / 16;
-            uint8_t* d = sQ + C::QSF * 16384 + hr * 64 + ((ct ^ ((hr >> 1) & 3)) << 4) + sub;
-            *reinterpret_cast<uint2*>(d) = H;
-            *reinterpret_cast<uint2*>(d + C::QPIECE) = L;
+            for (int x = 0; x < 4; ++x)
+              amax = fmaxf(amax, fmaxf(__uint_as_float((w[x] & 0x7fffu) << 16), __uint_as_float(w[x] & 0x7fff0000u)));
+          }
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+          const int e = pow2_exponent(amax);
+          const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+          if (lane == 0) sE[rr] = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+          for (int u = 0; u < QV; ++u) {
+            const int col = (u * 32 + lane) * 8;
+            if (col >= C::NF * 128 + C::TAIL * 64) continue;   // columns DK.. of the last atom are written as zeros
+            const uint32_t w[4] = {v[i][u].x, v[i][u].y, v[i][u].z, v[i][u].w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              split2(__uint_as_float(w[x] << 16) * inv, __uint_as_float(w[x] & 0xffff0000u) * inv, hi[x], lo[x]);
+            const uint2 Hi = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+            const uint2 Lo = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+            const int c16 = (col % 128) / 16, sub = col % 16;
+            if (col < C::QT) {
+              // staged in the P buffers: [term][atom][64 rows x 128 bytes]
+              uint8_t* d = sP + (col / 128) * (kM * 128) + rr * 128 + ((c16 ^ (rr & 7)) << 4) + sub;
+              *reinterpret_cast<uint2*>(d) = Hi;
+              *reinterpret_cast<uint2*>(d + (C::QT / 128) * (kM * 128)) = Lo;
+            } else if (col < C::NF * 128) {
+              uint8_t* d = sQ + ((col - C::QT) / 128) * (kM * 128) + rr * 128 + ((c16 ^ (rr & 7)) << 4) + sub;
+              *reinterpret_cast<uint2*>(d) = Hi;
+              *reinterpret_cast<uint2*>(d + C::QPIECE) = Lo;
+            } else {
+              const int ct = (col - C::NF * 128) / 16;
+              uint8_t* d = sQ + C::QSF * (kM * 128) + rr * 64 + ((ct ^ ((rr >> 1) & 3)) << 4) + sub;
+              *reinterpret_cast<uint2*>(d) = Hi;
+              *reinterpret_cast<uint2*>(d + C::QPIECE) = Lo;
+            }
           }
         }
       }
     }
-    softmax_sync();
+    bar_sync(1, 256);
     if (nchunks > 0) {
-      f_h = sM[h];
+      f_h = sE[r];
       if constexpr (C::QT > 0) {
-        // this group's term (0: hi, 1: lo) of row h into TMEM
+        // this side's term (0: hi, 1: lo) of row r into TMEM, in both lane halves
 #pragma unroll
         for (int a = 0; a < C::QT / 128; ++a) {
           uint32_t v[32];
-          const uint8_t* src = stage + (grp * (C::QT / 128) + a) * C::ATOM + h * 128;
+          const uint8_t* src = sP + (c * (C::QT / 128) + a) * (kM * 128) + r * 128;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const uint4 x = *reinterpret_cast<const uint4*>(src + ((c ^ (h & 7)) << 4));
-            v[4 * c] = x.x; v[4 * c + 1] = x.y; v[4 * c + 2] = x.z; v[4 * c + 3] = x.w;
+          for (int x = 0; x < 8; ++x) {
+            const uint4 w = *reinterpret_cast<const uint4*>(src + ((x ^ (r & 7)) << 4));
+            v[4 * x] = w.x; v[4 * x + 1] = w.y; v[4 * x + 2] = w.z; v[4 * x + 3] = w.w;
           }
-          tmem_st32(tmem + lane_addr + C::QCOL + grp * (C::QT / 4) + a * 32, v);
+          tmem_st32(tmem + lane_addr + C::QCOL + c * (C::QT / 4) + a * 32, v);
         }
         tmem_wait_st();
       }
@@ -474,156 +546,145 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
       __syncwarp();
       if (lane == 0) mbar_arrive(q_ready);
     }
-    softmax_sync();                                      // sM is read: it holds the reference from here on
-    float R = -INFINITY, l = 0.f;                        // l: this group's chunks' share of the row sum
+    bar_sync(1, 256);                                    // the staged terms are read: the P buffers are free
+    float R = -INFINITY, l = 0.f;                        // l: this thread's keys' share of the row sum
     bool ok = true;
-    for (int j = grp; j < nchunks; j += 2) {
+    // a failed wait leaves the loop running without waits: the warps of a
+    // barrier all arrive
+    for (int j = 0; j < nchunks; ++j) {
+      const int pb = j & 1;
       const uint32_t ph = (uint32_t)(j / 2) & 1;
-      // 1. the chunk's 64 scaled logits and their maximum
-      if (!wwait(&par_full[grp], ph)) { fail(7); ok = false; break; }
-      if (!wwait(&s_full[grp], ph)) { fail(8); ok = false; break; }
+      // 1. 32 scaled logits and their maximum
+      if (ok && !wwait(&par_full[pb], ph)) { fail(7); ok = false; }
+      if (ok && !wwait(&s_full[pb], ph)) { fail(8); ok = false; }
       tc_fence_after();
-      const uint32_t saddr = tmem + lane_addr + C::SCOL + grp * kN;
-      uint32_t s0[32], s1[32];
-      tmem_ld32(saddr, s0);
-      tmem_ld32(saddr + 32, s1);
-      tmem_wait_ld_dep(s0);
-      tmem_wait_ld_dep(s1);
-      const float2* par = sPar + grp * kN;
-      const float* inv = sInv + grp * kN;
+      uint32_t s[32];
+      tmem_ld32(tmem + lane_addr + C::SCOL + pb * (kN / 2) + c * 32, s);
+      tmem_wait_ld_dep(s);
+      const int key0 = pb * kN + kg * 64 + c * 32;
+      const float4* par = reinterpret_cast<const float4*>(sPar + key0);
       float cm = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float2 a0 = par[i], a1 = par[32 + i];
-        const float x0 = fmaf(__uint_as_float(s0[i]) * f_h, a0.x, a0.y);
-        const float x1 = fmaf(__uint_as_float(s1[i]) * f_h, a1.x, a1.y);
-        s0[i] = __float_as_uint(x0);
-        s1[i] = __float_as_uint(x1);
+      for (int i = 0; i < 16; ++i) {
+        const float4 a = par[i];
+        const float x0 = fmaf(__uint_as_float(s[2 * i]) * f_h, a.x, a.y);
+        const float x1 = fmaf(__uint_as_float(s[2 * i + 1]) * f_h, a.z, a.w);
+        s[2 * i] = __float_as_uint(x0);
+        s[2 * i + 1] = __float_as_uint(x1);
         cm = fmaxf(cm, fmaxf(x0, x1));
       }
-      // 2. the reference after the chunk before this one, and after this one
-      float Rp = -INFINITY;
-      if (j > 0) {
-        if (!wwait(&m_bar[(grp ^ 1) * 4 + quarter], (uint32_t)((j - 1) / 2) & 1)) { fail(9); ok = false; break; }
-        Rp = sM[h];
+      // 2. the row's maximum over its four threads, and the reference
+      float* mx = sMx + pb * 4 * kM + r;
+      mx[(kg * 2 + c) * kM] = cm;
+      bar_sync(2 + (quarter & 1), 128);
+      const float m = fmaxf(fmaxf(mx[0], mx[kM]), fmaxf(mx[2 * kM], mx[3 * kM]));
+      float Rn = R;
+      if (R == -INFINITY) {
+        if (m != -INFINITY) Rn = m - kHead;
+      } else if (m - kHead > R + kSlack) {
+        Rn = m - kHead;
       }
-      float Rn = Rp;
-      if (Rp == -INFINITY) {
-        if (cm != -INFINITY) Rn = cm - kHead;
-      } else if (cm - kHead > Rp + kSlack) {
-        Rn = cm - kHead;
-      }
-      sM[h] = Rn;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&m_bar[grp * 4 + quarter]);
-      const bool moved = Rp != -INFINITY && Rn != Rp;
-      if (R != Rn) {
-        l = R == -INFINITY ? 0.f : l * exp2f(R - Rn);
-        R = Rn;
-      }
-      // 3. the accumulator follows, once the P V before this chunk has landed
+      const bool moved = R != -INFINITY && Rn != R;
+      // 3. the accumulator follows, once the P V before this chunk is done:
+      //    that of an even chunk's predecessor is (its q K^T came after it)
       if (__any_sync(0xffffffffu, moved)) {
-        if (!wwait(&kv_empty[(j - 1) % kSlots], (uint32_t)((j - 1) / kSlots) & 1)) { fail(10); ok = false; break; }
+        if (ok && (j & 1) && !wwait(&kv_empty[2 * ((j - 1) & 1) + 1], (uint32_t)((j - 1) / 2) & 1)) { fail(10); ok = false; }
         tc_fence_after();
-        const float alpha = moved ? exp2f(Rp - Rn) : 1.f;
-        for (int c = 0; c < C::DVH / 32; ++c) {
-          uint32_t o[32];
-          const uint32_t oaddr = tmem + lane_addr + C::OCOL + c * 32;
-          tmem_ld32(oaddr, o);
-          tmem_wait_ld_dep(o);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-          tmem_st32(oaddr, o);
-        }
+        const float alpha = moved ? exp2f(R - Rn) : 1.f;
+        l *= alpha;
+        constexpr int W = C::OCOLS / 2 < 32 ? 16 : 32;
+#pragma unroll 1
+        for (int x = 0; x < C::OCOLS / 2; x += W)
+          tmem_scale<W>(tmem + lane_addr + C::OCOL + c * (C::OCOLS / 2) + x, alpha);
         tmem_wait_st();
       }
-      // 4. P in two terms: columns [0, 16) hi, [16, 32) lo of the S buffer
-      const float nR = Rn == -INFINITY ? 0.f : -Rn;
-      uint32_t pk[32];
+      R = Rn;
+      // 4. P in two terms, to shared memory (free: the q K^T of this chunk
+      //    came after the P V that read the buffer)
+      const float nR = R == -INFINITY ? 0.f : -R;
+      const float4* inv = reinterpret_cast<const float4*>(sInv + key0);
+      uint8_t* prow = sP + pb * 2 * C::PTERM + r * 128;
       float rs0 = 0.f, rs1 = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        uint32_t hi[2], lo[2];
+      for (int g = 0; g < 2; ++g) {
+        uint32_t hw[4], lw[4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int k0 = 4 * i + 2 * u;
-          const float x0 = __uint_as_float(k0 < 32 ? s0[k0 & 31] : s1[k0 & 31]);
-          const float x1 = __uint_as_float(k0 < 32 ? s0[(k0 + 1) & 31] : s1[(k0 + 1) & 31]);
-          const float e0 = ex2_approx(x0 + nR), e1 = ex2_approx(x1 + nR);
-          rs0 = fmaf(e0, inv[k0], rs0);
-          rs1 = fmaf(e1, inv[k0 + 1], rs1);
-          split2(e0, e1, hi[u], lo[u]);
+        for (int i = 0; i < 4; ++i) {
+          const float4 iv = inv[4 * g + i];
+          const int k0 = 16 * g + 4 * i;
+          const float e0 = ex2_approx(__uint_as_float(s[k0]) + nR), e1 = ex2_approx(__uint_as_float(s[k0 + 1]) + nR);
+          const float e2 = ex2_approx(__uint_as_float(s[k0 + 2]) + nR), e3 = ex2_approx(__uint_as_float(s[k0 + 3]) + nR);
+          rs0 = fmaf(e0, iv.x, rs0);
+          rs1 = fmaf(e1, iv.y, rs1);
+          rs0 = fmaf(e2, iv.z, rs0);
+          rs1 = fmaf(e3, iv.w, rs1);
+          uint32_t h0, l0, h1, l1;
+          split2(e0, e1, h0, l0);
+          split2(e2, e3, h1, l1);
+          hw[i] = h0 | (h1 << 16);
+          lw[i] = l0 | (l1 << 16);
         }
-        pk[i] = hi[0] | (hi[1] << 16);
-        pk[16 + i] = lo[0] | (lo[1] << 16);
+        uint8_t* d = prow + (((kg * 4 + c * 2 + g) ^ (r & 7)) << 4);
+        *reinterpret_cast<uint4*>(d) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+        *reinterpret_cast<uint4*>(d + C::PTERM) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
       }
       l += rs0 + rs1;
-      tmem_st32(saddr, pk);
-      tmem_wait_st();
+      fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&par_empty[grp]);
-        mbar_arrive(&p_full[grp]);
+        mbar_arrive(&par_empty[pb]);
+        mbar_arrive(&p_full[pb]);
       }
     }
-    // 5. output: both groups' sums at the last reference, then each group
-    //    writes half of this CTA's value columns
-    float Rl = -INFINITY;
-    if (ok && nchunks > 0) {
-      const int last = nchunks - 1;
-      if ((last & 1) != grp && !wwait(&m_bar[(last & 1) * 4 + quarter], (uint32_t)(last / 2) & 1)) {
-        fail(11);
-        ok = false;
-      }
-      if (ok && !wwait(&kv_empty[last % kSlots], (uint32_t)(last / kSlots) & 1)) {
-        fail(12);
-        ok = false;
-      }
-      if (ok) {
-        tc_fence_after();
-        Rl = sM[h];
-        if (R != Rl) l = R == -INFINITY ? 0.f : l * exp2f(R - Rl);
-      }
+    // 5. output: the row's sum over its four threads, then each thread a
+    //    quarter of the row's value columns
+    float* xl = sMx + (nchunks & 1) * 4 * kM + r;        // read last in chunk nchunks - 2
+    xl[(kg * 2 + c) * kM] = l;
+    bar_sync(2 + (quarter & 1), 128);
+    l = (xl[0] + xl[kM]) + (xl[2 * kM] + xl[3 * kM]);
+    if (ok && nchunks > 0 && !wwait(&kv_empty[2 * ((nchunks - 1) & 1) + 1], (uint32_t)((nchunks - 1) / 2) & 1)) {
+      fail(12);
+      ok = false;
     }
-    float* xl = reinterpret_cast<float*>(sKV);           // the ring is no longer read
-    softmax_sync();
-    if (ok && nchunks > 0) xl[grp * 128 + h] = l;
-    softmax_sync();
-    if (ok && nchunks > 0) l += xl[(grp ^ 1) * 128 + h];
     if (ok) {
+      tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      const float lse2 = l > 0.f ? Rl + log2f(l) : -INFINITY;
-      constexpr int OH = C::DVH / 2;                     // value columns per group
+      const float lse2 = l > 0.f ? R + log2f(l) : -INFINITY;
       const size_t orow = p.nsplit == 1 ? (size_t)row : (size_t)row * p.nsplit + split;
       if (nchunks > 0) {
-        const int v0 = half * C::DVH + grp * OH;
+        constexpr int W = C::OCOLS / 2 < 32 ? 16 : 32;
+        // TMEM column x of the accumulator: MMA x / (NV/2), its columns
+        // [kg NV/2, + NV/2) in this lane half
 #pragma unroll 1
-        for (int c = 0; c < OH / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tmem + lane_addr + C::OCOL + grp * OH + c * 32, o);
+        for (int x0 = 0; x0 < C::OCOLS / 2; x0 += W) {
+          const int x = c * (C::OCOLS / 2) + x0;
+          const int v0 = x / (C::NV / 2) * C::NV + kg * (C::NV / 2) + x % (C::NV / 2);
+          uint32_t o[W];
+          if constexpr (W == 32) tmem_ld32(tmem + lane_addr + C::OCOL + x, o);
+          else tmem_ld16(tmem + lane_addr + C::OCOL + x, o);
           tmem_wait_ld_dep(o);
           if (head_ok && p.nsplit == 1) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + (orow * p.H + h) * DV + v0 + c * 32);
+            uint4* dst = reinterpret_cast<uint4*>(p.out + (orow * p.H + h) * DV + v0);
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
+            for (int g = 0; g < W / 8; ++g) {
               uint32_t w[4];
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
-                w[x] = pack_bf16x2(__uint_as_float(o[8 * g + 2 * x]) * inv, __uint_as_float(o[8 * g + 2 * x + 1]) * inv);
+              for (int y = 0; y < 4; ++y)
+                w[y] = pack_bf16x2(__uint_as_float(o[8 * g + 2 * y]) * inv, __uint_as_float(o[8 * g + 2 * y + 1]) * inv);
               dst[g] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           } else if (head_ok) {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + (orow * p.H + h) * DV + v0 + c * 32);
+            float4* dst = reinterpret_cast<float4*>(p.part_o + (orow * p.H + h) * DV + v0);
 #pragma unroll
-            for (int g = 0; g < 8; ++g)
+            for (int g = 0; g < W / 4; ++g)
               dst[g] = make_float4(__uint_as_float(o[4 * g]) * inv, __uint_as_float(o[4 * g + 1]) * inv,
                                    __uint_as_float(o[4 * g + 2]) * inv, __uint_as_float(o[4 * g + 3]) * inv);
           }
           __syncwarp();
         }
       }
-      if (half == 0 && grp == 0 && head_ok) {
+      if (kg == 0 && c == 0 && head_ok) {
         if (p.nsplit == 1) {
           if (p.lse != nullptr) p.lse[orow * p.H + h] = lse2 * 0.6931471805599453f;
         } else {
@@ -678,7 +739,7 @@ cudaError_t launch_t(const LaunchCtx& c, const Params& p) {
   using C = Cfg<DK, DV>;
   cudaError_t e = cudaFuncSetAttribute(attn8_kernel<DK, DV, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
   if (e != cudaSuccess) return e;
-  attn8_kernel<DK, DV, PAGED><<<(unsigned)((long long)p.rows * p.nsplit * C::NHALF), kThreads, C::BYTES, c.stream>>>(p);
+  attn8_kernel<DK, DV, PAGED><<<(unsigned)((long long)p.rows * p.nsplit * p.hsplit), kThreads, C::BYTES, c.stream>>>(p);
   note_launches(1);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.nsplit == 1) return e;
@@ -690,8 +751,8 @@ cudaError_t launch_t(const LaunchCtx& c, const Params& p) {
 
 // Key splits per query row: one wave of CTAs (one per SM) when there are
 // fewer rows than SMs, never less than one chunk to a split.
-int choose_nsplit(long long rows, int d_v, long long slots, int num_sms) {
-  const long long ctas = rows * (d_v >= 128 ? 2 : 1);
+int choose_nsplit(long long rows, int H, long long slots, int num_sms) {
+  const long long ctas = rows * ((H + kM - 1) / kM);
   const long long chunks = (slots + kN - 1) / kN;
   long long n = num_sms / ctas;
   if (n < 1) n = 1;
@@ -707,8 +768,8 @@ size_t part_bytes(long long rows, int H, int d_v, int nsplit) {
 // Workspace of the attention over an 8-bit cache, for sparse and dense calls.
 size_t attn8_workspace_bytes(const Attn8Args& a, int num_sms) {
   const long long rows = (long long)a.B * a.T;
-  const size_t s = part_bytes(rows, a.H, a.d_v, choose_nsplit(rows, a.d_v, a.k, num_sms));
-  const size_t d = part_bytes(rows, a.H, a.d_v, choose_nsplit(rows, a.d_v, a.S, num_sms));
+  const size_t s = part_bytes(rows, a.H, a.d_v, choose_nsplit(rows, a.H, a.k, num_sms));
+  const size_t d = part_bytes(rows, a.H, a.d_v, choose_nsplit(rows, a.H, a.S, num_sms));
   return ((s > d ? s : d) + 255) / 256 * 256;
 }
 
@@ -727,7 +788,8 @@ cudaError_t launch_attn8(const LaunchCtx& c, const Attn8Args& a) {
   p.k = a.k;
   const long long rows = (long long)a.B * a.T;
   p.rows = (int)rows;
-  p.nsplit = choose_nsplit(rows, a.d_v, a.idx != nullptr ? a.k : a.S, c.num_sms);
+  p.nsplit = choose_nsplit(rows, a.H, a.idx != nullptr ? a.k : a.S, c.num_sms);
+  p.hsplit = (a.H + kM - 1) / kM;
   p.scale_log2 = a.tau * 1.4426950408889634f;
   p.wait_ns = c.wait_ns;
   p.err = c.err;
