@@ -110,7 +110,12 @@ struct Params {
   int dense_rows;        // rows with t < dense_rows take keys 0..pos(t), idx unread
   uint16_t* out;
   float* lse;
-  float* part_o;         // [rows, nsplit, H, d_v] (nsplit > 1), normalised by the part's own l
+  // nsplit > 1: the parts' outputs, normalised by their own l, as FP16 times
+  // one FP32 factor per 32 columns (16 at d_v 64): a group's largest is 2^14
+  // or more, so its values keep FP16's 11 bits down to 2^-28 of it, whatever
+  // the cache's scales
+  __half* part_o;        // [rows, nsplit, H, d_v]
+  float* part_f;         // [rows, nsplit, H, d_v / 32 (16)]
   float* part_lse;       // [rows, nsplit, H], log2 units
   int T, H, k;
   int rows, nsplit, hsplit;
@@ -160,23 +165,116 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// W columns of TMEM times alpha (32 lanes of one warp)
+// asynchronous copy of `bytes` (a multiple of 16) from shared to global memory
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+
+// largest magnitude of eight BF16 numbers, as its bits
+__device__ __forceinline__ uint32_t max_abs8(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+  return m;
+}
+
+// W columns of TMEM times alpha (32 lanes of one warp), 64 in flight
 template <int W>
 __device__ __forceinline__ void tmem_scale(uint32_t addr, float alpha) {
-  if constexpr (W == 32) {
-    uint32_t o[32];
-    tmem_ld32(addr, o);
-    tmem_wait_ld_dep(o);
+  if constexpr (W >= 64) {
+#pragma unroll 1
+    for (int x = 0; x < W; x += 64) {
+      uint32_t o0[32], o1[32];
+      tmem_ld32(addr + x, o0);
+      tmem_ld32(addr + x + 32, o1);
+      tmem_wait_ld_dep(o0);
+      tmem_wait_ld_dep(o1);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-    tmem_st32(addr, o);
+      for (int i = 0; i < 32; ++i) o0[i] = __float_as_uint(__uint_as_float(o0[i]) * alpha);
+      tmem_st32(addr + x, o0);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o1[i] = __float_as_uint(__uint_as_float(o1[i]) * alpha);
+      tmem_st32(addr + x + 32, o1);
+    }
   } else {
+    static_assert(W == 16, "columns");
     uint32_t o[16];
     tmem_ld16(addr, o);
     tmem_wait_ld_dep(o);
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
     tmem_st16(addr, o);
+  }
+  tmem_wait_st();
+}
+
+// Four head rows of q (rows 4 w .. 4 w + 3 of the CTA's 64) in two e4m3 terms:
+// the rows are contiguous, so a warp takes them in full steps of 32 vectors of
+// eight columns; a row's exponent comes from its maximum over the warp.
+template <int DK>
+struct QRows {
+  static constexpr int VPR = DK / 8, NVEC = 4 * VPR, STEPS = (NVEC + 31) / 32;
+  uint4 v[STEPS];
+};
+template <int DK>
+__device__ __forceinline__ void load_q_rows(QRows<DK>& q4, const uint16_t* q, int heads, int w, int lane) {
+  using Q = QRows<DK>;
+#pragma unroll
+  for (int s = 0; s < Q::STEPS; ++s) {
+    const int i = s * 32 + lane;
+    q4.v[s] = make_uint4(0u, 0u, 0u, 0u);
+    if (i < Q::NVEC && 4 * w + i / Q::VPR < heads)
+      q4.v[s] = __ldg(reinterpret_cast<const uint4*>(q + (size_t)4 * w * DK) + i);
+  }
+}
+template <int DK, int DV>
+__device__ __forceinline__ void split_q_rows(const QRows<DK>& q4, int w, int lane, uint8_t* sQ, uint8_t* sP, float* sE) {
+  using C = Cfg<DK, DV>;
+  constexpr int VPR = QRows<DK>::VPR, NVEC = QRows<DK>::NVEC, STEPS = QRows<DK>::STEPS;
+  const uint4* v = q4.v;
+  uint32_t m[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    const uint32_t x = max_abs8(v[s]);
+    const int row = (s * 32 + lane) / VPR;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i >= s * 32 / VPR && i <= (s * 32 + 31) / VPR) m[i] = max(m[i], row == i ? x : 0u);
+  }
+  float inv[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = pow2_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, m[i]) << 16));
+    inv[i] = __uint_as_float((uint32_t)(127 - e) << 23);
+    if (lane == i) sE[4 * w + i] = __uint_as_float((uint32_t)(127 + e) << 23);
+  }
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    const int i = s * 32 + lane, row = i / VPR, col = (i - row * VPR) * 8;
+    if (i >= NVEC) continue;
+    const float f = row == 0 ? inv[0] : row == 1 ? inv[1] : row == 2 ? inv[2] : inv[3];
+    const uint32_t x[4] = {v[s].x, v[s].y, v[s].z, v[s].w};
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) split2(__uint_as_float(x[y] << 16) * f, __uint_as_float(x[y] & 0xffff0000u) * f, hi[y], lo[y]);
+    const int rr = 4 * w + row, c16 = (col % 128) / 16, sub = col % 16;
+    uint8_t* d;
+    int to_lo;                                           // distance to the second term
+    if (col < C::QT) {
+      // staged in the P buffers: [term][atom][64 rows x 128 bytes]
+      d = sP + (col / 128) * (kM * 128) + rr * 128 + ((c16 ^ (rr & 7)) << 4) + sub;
+      to_lo = (C::QT / 128) * (kM * 128);
+    } else if (col < C::NF * 128) {
+      d = sQ + ((col - C::QT) / 128) * (kM * 128) + rr * 128 + ((c16 ^ (rr & 7)) << 4) + sub;
+      to_lo = C::QPIECE;
+    } else {
+      d = sQ + C::QSF * (kM * 128) + rr * 64 + ((((col - C::NF * 128) / 16) ^ ((rr >> 1) & 3)) << 4) + sub;
+      to_lo = C::QPIECE;
+    }
+    *reinterpret_cast<uint2*>(d) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+    *reinterpret_cast<uint2*>(d + to_lo) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
   }
 }
 
@@ -189,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     if (threadIdx.x == 0) report_error(p.err, DSA_ERR_DEVICE_BOUNDS, ERR_SITE_ATTN8 | (0xAu << 8));
     return;
   }
+  pdl_launch_dependents();                     // the combine may be scheduled; it waits for this grid
   uint8_t* sQ = smem + C::OFF_Q;
   uint8_t* sKV = smem + C::OFF_KV;
   uint8_t* sP = smem + C::OFF_P;
@@ -222,6 +321,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
   const int slot0 = min(split * kc, nslots), slot1 = min(slot0 + kc, nslots);
   const int nchunks = (slot1 - slot0 + kN - 1) / kN;
 
+  // the softmax warps' rows of q (0..31) are on their way while the barriers
+  // and TMEM are set up; the gather warps take rows 32..63 behind their first
+  // chunk
+  QRows<DK> q4;
+  const uint16_t* q0 = p.q + ((size_t)row * p.H + hs * kM) * DK;
+  if (warp >= kFirstSoftmax && warp < kFirstGather) load_q_rows(q4, q0, p.H - hs * kM, warp - kFirstSoftmax, lane);
+
   if (threadIdx.x == 0) {
     mbar_init(q_ready, 8);
     for (int i = 0; i < 2; ++i) {
@@ -242,11 +348,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     tmem_relinquish();
   }
   if constexpr (DK % 128 != 0 && C::TAIL == 0) {
-    // columns DK.. of the keys' atom meet zero columns of q in the last K
-    // step: they must not hold NaN bytes
-    for (int i = threadIdx.x; i < 2 * kN * 8; i += kThreads)
-      if (i % 8 >= DK / 16)
-        *reinterpret_cast<uint4*>(sKV + (i / 8) * 128 + (((i % 8) ^ ((i / 8) & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+    // columns DK.. of the atoms of q (rows 0..127: both terms) and of the keys
+    for (int i = threadIdx.x; i < 2 * (kM + kN) * 8; i += kThreads) {
+      const int rr = i / 8;
+      uint8_t* d = rr < 2 * kM ? sQ + rr * 128 : sKV + (rr - 2 * kM) * 128;
+      if (i % 8 >= DK / 16) *reinterpret_cast<uint4*>(d + (((i % 8) ^ (rr & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+    }
     fence_proxy_async_smem();
   }
   tc_fence_before();
@@ -283,6 +390,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     const int kl = 16 * g + (lane & 15);
     int r_cur = row_of(load_idx(slot0 + kl));
     int i_next = load_idx(slot0 + kN + kl);
+    // this warp's rows of q, behind the first chunk
+    auto help_q = [&]() {
+      load_q_rows(q4, q0, p.H - hs * kM, warp - kFirstSoftmax, lane);
+      split_q_rows<DK, DV>(q4, warp - kFirstSoftmax, lane, sQ, sP, sE);
+      fence_proxy_async_smem();
+      asm volatile("bar.arrive 1, 512;" ::: "memory");
+    };
     for (int j = 0; j < nchunks; ++j) {
       const int rg = j & 1;
       if (j >= 2 && !wwait(&kv_empty[2 * rg + g / 4], (uint32_t)(j / 2 - 1) & 1)) { fail(1); break; }
@@ -313,7 +427,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
       }
       cp_async_arrive(&kv_full[rg]);
       r_cur = r_next;
+      if (j == 0) help_q();
     }
+    if (nchunks == 0) help_q();
     cp_async_commit();
     cp_async_wait<0>();
   } else if (warp == kParamWarp) {
@@ -459,71 +575,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     const int h = hs * kM + r;
     const bool head_ok = h < p.H;
     float f_h = 0.f;
-    if (nchunks > 0) {
-      // q rows: a warp takes 8 rows, four in flight; the row's exponent from
-      // its maximum, then the two terms of eight columns per lane and step
-      constexpr int QV = (DK + 255) / 256;               // 8-column vectors per lane
-      constexpr int QR = 4;
-#pragma unroll 1
-      for (int i0 = 0; i0 < 8; i0 += QR) {
-        uint4 v[QR][QV];
-#pragma unroll
-        for (int i = 0; i < QR; ++i)
-#pragma unroll
-          for (int u = 0; u < QV; ++u) {
-            const int hr = hs * kM + sw * 8 + i0 + i, col = (u * 32 + lane) * 8;
-            v[i][u] = make_uint4(0u, 0u, 0u, 0u);
-            if (hr < p.H && col < DK)
-              v[i][u] = __ldg(reinterpret_cast<const uint4*>(p.q + ((size_t)row * p.H + hr) * DK + col));
-          }
-#pragma unroll
-        for (int i = 0; i < QR; ++i) {
-          const int rr = sw * 8 + i0 + i;
-          float amax = 0.f;
-#pragma unroll
-          for (int u = 0; u < QV; ++u) {
-            const uint32_t w[4] = {v[i][u].x, v[i][u].y, v[i][u].z, v[i][u].w};
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              amax = fmaxf(amax, fmaxf(__uint_as_float((w[x] & 0x7fffu) << 16), __uint_as_float(w[x] & 0x7fff0000u)));
-          }
-#pragma unroll
-          for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-          const int e = pow2_exponent(amax);
-          const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-          if (lane == 0) sE[rr] = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-          for (int u = 0; u < QV; ++u) {
-            const int col = (u * 32 + lane) * 8;
-            if (col >= C::NF * 128 + C::TAIL * 64) continue;   // columns DK.. of the last atom are written as zeros
-            const uint32_t w[4] = {v[i][u].x, v[i][u].y, v[i][u].z, v[i][u].w};
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              split2(__uint_as_float(w[x] << 16) * inv, __uint_as_float(w[x] & 0xffff0000u) * inv, hi[x], lo[x]);
-            const uint2 Hi = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-            const uint2 Lo = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-            const int c16 = (col % 128) / 16, sub = col % 16;
-            if (col < C::QT) {
-              // staged in the P buffers: [term][atom][64 rows x 128 bytes]
-              uint8_t* d = sP + (col / 128) * (kM * 128) + rr * 128 + ((c16 ^ (rr & 7)) << 4) + sub;
-              *reinterpret_cast<uint2*>(d) = Hi;
-              *reinterpret_cast<uint2*>(d + (C::QT / 128) * (kM * 128)) = Lo;
-            } else if (col < C::NF * 128) {
-              uint8_t* d = sQ + ((col - C::QT) / 128) * (kM * 128) + rr * 128 + ((c16 ^ (rr & 7)) << 4) + sub;
-              *reinterpret_cast<uint2*>(d) = Hi;
-              *reinterpret_cast<uint2*>(d + C::QPIECE) = Lo;
-            } else {
-              const int ct = (col - C::NF * 128) / 16;
-              uint8_t* d = sQ + C::QSF * (kM * 128) + rr * 64 + ((ct ^ ((rr >> 1) & 3)) << 4) + sub;
-              *reinterpret_cast<uint2*>(d) = Hi;
-              *reinterpret_cast<uint2*>(d + C::QPIECE) = Lo;
-            }
-          }
-        }
-      }
-    }
-    bar_sync(1, 256);
+    split_q_rows<DK, DV>(q4, sw, lane, sQ, sP, sE);
+    fence_proxy_async_smem();
+    bar_sync(1, 512);                                    // with the gather warps' rows
     if (nchunks > 0) {
       f_h = sE[r];
       if constexpr (C::QT > 0) {
@@ -541,12 +595,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
         }
         tmem_wait_st();
       }
-      fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_ready);
     }
-    bar_sync(1, 256);                                    // the staged terms are read: the P buffers are free
+    bar_sync(4, 256);                                    // the staged terms are read: the P buffers are free
     float R = -INFINITY, l = 0.f;                        // l: this thread's keys' share of the row sum
     bool ok = true;
     // a failed wait leaves the loop running without waits: the warps of a
@@ -585,21 +638,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
         Rn = m - kHead;
       }
       const bool moved = R != -INFINITY && Rn != R;
-      // 3. the accumulator follows, once the P V before this chunk is done:
-      //    that of an even chunk's predecessor is (its q K^T came after it)
-      if (__any_sync(0xffffffffu, moved)) {
-        if (ok && (j & 1) && !wwait(&kv_empty[2 * ((j - 1) & 1) + 1], (uint32_t)((j - 1) / 2) & 1)) { fail(10); ok = false; }
-        tc_fence_after();
-        const float alpha = moved ? exp2f(R - Rn) : 1.f;
-        l *= alpha;
-        constexpr int W = C::OCOLS / 2 < 32 ? 16 : 32;
-#pragma unroll 1
-        for (int x = 0; x < C::OCOLS / 2; x += W)
-          tmem_scale<W>(tmem + lane_addr + C::OCOL + c * (C::OCOLS / 2) + x, alpha);
-        tmem_wait_st();
-      }
+      const float alpha = moved ? exp2f(R - Rn) : 1.f;
+      l *= alpha;
       R = Rn;
-      // 4. P in two terms, to shared memory (free: the q K^T of this chunk
+      // 3. P in two terms, to shared memory (free: the q K^T of this chunk
       //    came after the P V that read the buffer)
       const float nR = R == -INFINITY ? 0.f : -R;
       const float4* inv = reinterpret_cast<const float4*>(sInv + key0);
@@ -630,6 +672,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
       }
       l += rs0 + rs1;
       fence_proxy_async_smem();
+      // 4. the accumulator follows the reference, once the P V before this
+      //    chunk is done (that of an even chunk's predecessor is: its q K^T
+      //    came after it)
+      if (__any_sync(0xffffffffu, moved)) {
+        if (ok && (j & 1) && !wwait(&kv_empty[2 * ((j - 1) & 1) + 1], (uint32_t)((j - 1) / 2) & 1)) { fail(10); ok = false; }
+        tc_fence_after();
+        tmem_scale<C::OCOLS / 2>(tmem + lane_addr + C::OCOL + c * (C::OCOLS / 2), alpha);
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -637,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
         mbar_arrive(&p_full[pb]);
       }
     }
-    // 5. output: the row's sum over its four threads, then each thread a
+    // output: the row's sum over its four threads, then each thread a
     //    quarter of the row's value columns
     float* xl = sMx + (nchunks & 1) * 4 * kM + r;        // read last in chunk nchunks - 2
     xl[(kg * 2 + c) * kM] = l;
@@ -647,49 +697,69 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
       fail(12);
       ok = false;
     }
-    if (ok) {
+    // The rows leave through the keys' regions (every MMA is done): a thread
+    // has 16-byte pieces of one row, which as stores of their own would touch
+    // 32 lines an instruction; a row goes out as one bulk copy.  The pitch
+    // keeps the pieces of eight rows on different banks.
+    constexpr int PITCH = DV * 2 + 16;
+    static_assert(kM * PITCH <= C::KV_BYTES, "output staging");
+    const bool write = ok && nchunks > 0;
+    const size_t orow = p.nsplit == 1 ? (size_t)row : (size_t)row * p.nsplit + split;
+    if (write) {
       tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      const float lse2 = l > 0.f ? R + log2f(l) : -INFINITY;
-      const size_t orow = p.nsplit == 1 ? (size_t)row : (size_t)row * p.nsplit + split;
-      if (nchunks > 0) {
-        constexpr int W = C::OCOLS / 2 < 32 ? 16 : 32;
-        // TMEM column x of the accumulator: MMA x / (NV/2), its columns
-        // [kg NV/2, + NV/2) in this lane half
+      constexpr int W = C::OCOLS / 2 < 32 ? 16 : 32;
+      // TMEM column x of the accumulator: MMA x / (NV/2), its columns
+      // [kg NV/2, + NV/2) in this lane half
 #pragma unroll 1
-        for (int x0 = 0; x0 < C::OCOLS / 2; x0 += W) {
-          const int x = c * (C::OCOLS / 2) + x0;
-          const int v0 = x / (C::NV / 2) * C::NV + kg * (C::NV / 2) + x % (C::NV / 2);
-          uint32_t o[W];
-          if constexpr (W == 32) tmem_ld32(tmem + lane_addr + C::OCOL + x, o);
-          else tmem_ld16(tmem + lane_addr + C::OCOL + x, o);
-          tmem_wait_ld_dep(o);
-          if (head_ok && p.nsplit == 1) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + (orow * p.H + h) * DV + v0);
+      for (int x0 = 0; x0 < C::OCOLS / 2; x0 += W) {
+        const int x = c * (C::OCOLS / 2) + x0;
+        const int v0 = x / (C::NV / 2) * C::NV + kg * (C::NV / 2) + x % (C::NV / 2);
+        uint32_t o[W];
+        if constexpr (W == 32) tmem_ld32(tmem + lane_addr + C::OCOL + x, o);
+        else tmem_ld16(tmem + lane_addr + C::OCOL + x, o);
+        tmem_wait_ld_dep(o);
+        uint8_t* dst = sKV + r * PITCH + v0 * 2;
+        float f = inv;
+        if (p.nsplit > 1) {
+          float mo = 0.f;
 #pragma unroll
-            for (int g = 0; g < W / 8; ++g) {
-              uint32_t w[4];
+          for (int i = 0; i < W; ++i) mo = fmaxf(mo, fabsf(__uint_as_float(o[i])));
+          // the power of two that brings the group's largest into [2^14, 2^15)
+          const int e = min(max(127 + 14 - (int)(__float_as_uint(mo * inv) >> 23), -120), 126);
+          f = inv * __uint_as_float((uint32_t)(127 + e) << 23);
+          if (head_ok) p.part_f[(orow * p.H + h) * (DV / W) + v0 / W] = __uint_as_float((uint32_t)(127 - e) << 23);
+        }
 #pragma unroll
-              for (int y = 0; y < 4; ++y)
-                w[y] = pack_bf16x2(__uint_as_float(o[8 * g + 2 * y]) * inv, __uint_as_float(o[8 * g + 2 * y + 1]) * inv);
-              dst[g] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          } else if (head_ok) {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + (orow * p.H + h) * DV + v0);
+        for (int g = 0; g < W / 8; ++g) {
+          uint32_t w[4];
 #pragma unroll
-            for (int g = 0; g < W / 4; ++g)
-              dst[g] = make_float4(__uint_as_float(o[4 * g]) * inv, __uint_as_float(o[4 * g + 1]) * inv,
-                                   __uint_as_float(o[4 * g + 2]) * inv, __uint_as_float(o[4 * g + 3]) * inv);
+          for (int y = 0; y < 4; ++y) {
+            const float o0 = __uint_as_float(o[8 * g + 2 * y]) * f, o1 = __uint_as_float(o[8 * g + 2 * y + 1]) * f;
+            w[y] = p.nsplit > 1 ? pack_f16x2(o0, o1) : pack_bf16x2(o0, o1);
           }
-          __syncwarp();
+          *reinterpret_cast<uint4*>(dst + 16 * g) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      if (kg == 0 && c == 0 && head_ok) {
-        if (p.nsplit == 1) {
-          if (p.lse != nullptr) p.lse[orow * p.H + h] = lse2 * 0.6931471805599453f;
-        } else {
-          p.part_lse[orow * p.H + h] = lse2;
-        }
+      fence_proxy_async_smem();
+    }
+    bar_sync(2 + (quarter & 1), 128);
+    if (write && kg == 0 && c == 0) {
+      // this warp's rows, one a lane
+      if (head_ok) {
+        void* dst = p.nsplit == 1 ? static_cast<void*>(p.out + (orow * p.H + h) * DV)
+                                  : static_cast<void*>(p.part_o + (orow * p.H + h) * DV);
+        bulk_store(dst, sKV + r * PITCH, DV * 2);
+      }
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    }
+    if (ok && kg == 0 && c == 0 && head_ok) {
+      const float lse2 = l > 0.f ? R + log2f(l) : -INFINITY;
+      if (p.nsplit == 1) {
+        if (p.lse != nullptr) p.lse[orow * p.H + h] = lse2 * 0.6931471805599453f;
+      } else {
+        p.part_lse[orow * p.H + h] = lse2;
       }
     }
   }
@@ -702,36 +772,62 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
   }
 }
 
-// Merge the key splits of each (row, head): weights 2^(lse_s - max).
+// Merge the key splits of each (row, head): weights 2^(lse_s - max).  A thread
+// takes four columns; the loads of up to eight splits are issued before the
+// first is used (one memory latency a batch).  128 threads of up to 80
+// registers fit beside an attention CTA, so that the blocks can wait there for its end.
+constexpr int kCombineThreads = 128;
 template <int DV>
-__global__ void __launch_bounds__(DV / 4) attn8_combine_kernel(const float* part_o, const float* part_lse,
-                                                               uint16_t* out, float* lse, int H, int nsplit) {
-  const size_t row = blockIdx.x / H;
-  const int h = blockIdx.x % H;
-  const float* ls = part_lse + row * nsplit * H + h;
-  const float* po = part_o + (row * nsplit * H + h) * DV + threadIdx.x * 4;
+__global__ void __launch_bounds__(kCombineThreads, 6) attn8_combine_kernel(const __half* part_o, const float* part_f,
+                                                            const float* part_lse, uint16_t* out, float* lse,
+                                                            long long heads, int H, int nsplit) {
+  constexpr int kBatch = 8, TPH = DV / 4, W = DV >= 128 ? 32 : 16;
+  pdl_wait();
+  const long long gh = (long long)blockIdx.x * (kCombineThreads / TPH) + threadIdx.x / TPH;
+  if (gh >= heads) return;
+  const long long row = gh / H;
+  const int h = (int)(gh - row * H), d0 = (threadIdx.x % TPH) * 4;
+  const long long first = row * nsplit * H + h;            // split s at + s H
   float mx = -INFINITY;
-  for (int s = 0; s < nsplit; ++s) mx = fmaxf(mx, ls[(size_t)s * H]);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float wsum = 0.f;
-  if (mx != -INFINITY) {
-    for (int s = 0; s < nsplit; ++s) {
-      const float l = ls[(size_t)s * H];
-      if (l == -INFINITY) continue;                      // an empty part's output was never written
-      const float w = exp2f(l - mx);
-      const float4 v = *reinterpret_cast<const float4*>(po + (size_t)s * H * DV);
+  if (nsplit > kBatch)
+    for (int s = 0; s < nsplit; ++s) mx = fmaxf(mx, part_lse[first + (long long)s * H]);
+  float acc[4] = {0.f, 0.f, 0.f, 0.f}, wsum = 0.f;
+  for (int s0 = 0; s0 < nsplit; s0 += kBatch) {
+    float l[kBatch], f[kBatch];
+    uint2 v[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const long long at = first + (long long)(s0 + i) * H;
+      l[i] = -INFINITY;
+      if (s0 + i < nsplit) {
+        l[i] = part_lse[at];
+        v[i] = *reinterpret_cast<const uint2*>(part_o + at * DV + d0);
+        f[i] = part_f[at * (DV / W) + d0 / W];
+      }
+    }
+    if (nsplit <= kBatch) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) mx = fmaxf(mx, l[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (l[i] == -INFINITY) continue;                     // an empty part's output was never written
+      const float w = exp2f(l[i] - mx);
       wsum += w;
-      acc.x = fmaf(w, v.x, acc.x);
-      acc.y = fmaf(w, v.y, acc.y);
-      acc.z = fmaf(w, v.z, acc.z);
-      acc.w = fmaf(w, v.w, acc.w);
+      const float wf = w * f[i];
+      const uint32_t u[2] = {v[i].x, v[i].y};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&u[c]));
+        acc[2 * c] = fmaf(wf, x.x, acc[2 * c]);
+        acc[2 * c + 1] = fmaf(wf, x.y, acc[2 * c + 1]);
+      }
     }
   }
   const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
-  *reinterpret_cast<uint2*>(out + (row * H + h) * DV + threadIdx.x * 4) =
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (threadIdx.x == 0 && lse != nullptr)
-    lse[row * H + h] = wsum > 0.f ? (mx + log2f(wsum)) * 0.6931471805599453f : -INFINITY;
+  *reinterpret_cast<uint2*>(out + gh * DV + d0) =
+      make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  if (d0 == 0 && lse != nullptr) lse[gh] = wsum > 0.f ? (mx + log2f(wsum)) * 0.6931471805599453f : -INFINITY;
 }
 
 template <int DK, int DV, bool PAGED>
@@ -743,10 +839,14 @@ cudaError_t launch_t(const LaunchCtx& c, const Params& p) {
   note_launches(1);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.nsplit == 1) return e;
-  attn8_combine_kernel<DV><<<(unsigned)((long long)p.rows * p.H), DV / 4, 0, c.stream>>>(p.part_o, p.part_lse, p.out,
-                                                                                       p.lse, p.H, p.nsplit);
+  // a programmatic dependent: its blocks may start while the attention drains
+  const long long heads = (long long)p.rows * p.H;
+  const int per = kCombineThreads / (DV / 4);
+  e = launch_pdl(attn8_combine_kernel<DV>, dim3((unsigned)((heads + per - 1) / per)), dim3(kCombineThreads), 0, c.stream,
+                 (const __half*)p.part_o, (const float*)p.part_f, (const float*)p.part_lse, p.out, p.lse, heads, p.H,
+                 p.nsplit);
   note_launches(1);
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 // Key splits per query row: one wave of CTAs (one per SM) when there are
@@ -759,8 +859,9 @@ int choose_nsplit(long long rows, int H, long long slots, int num_sms) {
   return (int)(n < chunks ? n : chunks);
 }
 
+// FP16 outputs, their factors (at most d_v / 16 a head) and log2-sum-exps
 size_t part_bytes(long long rows, int H, int d_v, int nsplit) {
-  return nsplit > 1 ? (size_t)rows * nsplit * H * (d_v + 1) * sizeof(float) : 0;
+  return nsplit > 1 ? (size_t)rows * nsplit * H * (d_v * 2 + d_v / 16 * 4 + 4) : 0;
 }
 
 }  // namespace
@@ -795,8 +896,10 @@ cudaError_t launch_attn8(const LaunchCtx& c, const Attn8Args& a) {
   p.err = c.err;
   if (p.nsplit > 1) {
     if (a.ws == nullptr) return cudaErrorInvalidValue;
-    p.part_o = static_cast<float*>(a.ws);
-    p.part_lse = p.part_o + (size_t)rows * p.nsplit * a.H * a.d_v;
+    const size_t n = (size_t)rows * p.nsplit * a.H;
+    p.part_o = static_cast<__half*>(a.ws);
+    p.part_f = reinterpret_cast<float*>(p.part_o + n * a.d_v);
+    p.part_lse = p.part_f + n * (a.d_v / 16);
   }
   const bool paged = a.map.page_size != 0;
   if (a.d_k == 576 && a.d_v == 512) return paged ? launch_t<576, 512, true>(c, p) : launch_t<576, 512, false>(c, p);
