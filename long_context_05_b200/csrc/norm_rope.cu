@@ -11,9 +11,11 @@
 //
 // Nothing is reused between rows but the angles of a token and the weights,
 // so the bound is HBM: 4 bytes per element forward, 6 backward.  A row is
-// held in the registers of G lanes (8 up to 576 columns: one 16-byte load per
-// lane covers 128 contiguous bytes of four rows per warp), read once, reduced
-// by shuffles and written once.  The r/2 sines and cosines of a token are
+// held in the registers of G lanes (16 up to 640 columns: a 16-byte load of
+// each covers 256 contiguous bytes of a row), read once, reduced by shuffles
+// and written once.  The pair of a rotated column comes from another lane by
+// shuffles where it lies in the same step of 16 G bytes, else it is read again
+// (from L1).  The r/2 sines and cosines of a token are
 // formed once per block, in shared memory, for all heads the block handles.
 // The angle is reduced in FP64 (pos times f is exact to 2^-53 there; FP32
 // would be off by 2^-24 of the whole angle, half a degree at position 128K),
@@ -33,7 +35,9 @@ constexpr int kTileTokens = 16;   // tokens whose angles a block holds at a time
 constexpr int kMaxHalf = 128;     // rotated pairs, at most (r <= 256)
 constexpr int kMaxD = 1024;
 
-enum RopeMode { kNone = 0, kHalf = 1, kInter = 2 };
+// kHalf: pairs (i, i + r/2), the partner read again; kShfl: the same with the
+// partner columns in lane ^ (r / 16) of the same step; kInter: pairs (2i, 2i + 1)
+enum RopeMode { kNone = 0, kHalf = 1, kInter = 2, kShfl = 3 };
 
 struct Side {
   const uint16_t* x;     // rows in [tokens, H, D]
@@ -98,7 +102,7 @@ __device__ __forceinline__ void fill_angles(const NrParams& p, float2* cs, int n
 }
 
 // Rotate the eight columns at `col` (offset rc = col - (D - r) >= 0 into the
-// rotated range).  kHalf: o holds the partner columns rc +- r/2.  back: by
+// rotated range).  kHalf, kShfl: o holds the partner columns rc +- r/2.  back: by
 // the opposite angle.
 template <int MODE>
 __device__ __forceinline__ void rotate8(float (&z)[8], const float (&o)[8], const float2* cs, int rc, int half,
@@ -112,7 +116,7 @@ __device__ __forceinline__ void rotate8(float (&z)[8], const float (&o)[8], cons
       z[2 * i] = u * a.x - v * s;
       z[2 * i + 1] = u * s + v * a.x;
     }
-  } else if constexpr (MODE == kHalf) {
+  } else if constexpr (MODE == kHalf || MODE == kShfl) {
     const bool first = rc < half;
     const float2* a0 = cs + (first ? rc : rc - half);
 #pragma unroll
@@ -183,13 +187,11 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(NrParams p) {
     for (int d = 1; d < G; d <<= 1) ss += __shfl_xor_sync(lane_grp, ss, d);
     __syncwarp(lane_grp);                         // every lane holds its columns: the row may be written over
     const float rho = rsqrtf(fmaf(ss, p.inv_norm, p.eps));
-    if (!on) continue;
     uint16_t* y = s.y + base;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int col = (j * G + gl) * 8;
-      if (col >= p.D) continue;
-      float f[8];
+      float f[8], g[8];
       unpack8(v[j], f);
       if (col < p.norm) {
         float w[8];
@@ -197,8 +199,15 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(NrParams p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] *= rho * w[i];
       }
+      if constexpr (MODE == kShfl) {
+        // every lane of the row takes part in a step that holds rotated columns
+        if ((j * G + G) * 8 > r0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) g[i] = __shfl_xor_sync(lane_grp, f[i], half >> 3);
+        }
+      }
+      if (!on || col >= p.D) continue;
       if (MODE != kNone && col >= r0) {
-        float g[8];
         if constexpr (MODE == kHalf) {
           const int pc = col - r0 < half ? col + half : col - half;
           unpack8(o[j], g);
@@ -219,9 +228,12 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(NrParams p) {
   }
 }
 
-// Backward.  A block keeps to one side and takes its items in turn.
+// Backward.  A block keeps to one side and takes its items in turn; the grid
+// is what is resident at once, so that every block has an equal share.
+template <int V>
+constexpr int bwd_blocks_per_sm() { return V >= 4 ? 3 : 6; }
 template <int G, int V, int MODE>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(NrParams p) {
+__global__ void __launch_bounds__(kThreads, bwd_blocks_per_sm<V>()) norm_rope_bwd_kernel(NrParams p) {
   extern __shared__ float2 cs[];
   constexpr int kRows = kThreads / G;
   const int gl = threadIdx.x % G, grp = threadIdx.x / G;
@@ -269,18 +281,27 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(NrParams p) {
       float ss = 0.f, dot = 0.f;
       auto rotated = [&](int j, int col, float (&f)[8]) {
         unpack8(g[j], f);
-        if (MODE != kNone && col >= r0) {
-          float q[8];
-          if constexpr (MODE == kHalf) unpack8(o[j], q);
-          rotate8<MODE>(f, q, cs + tt * half, col - r0, half, true);
+        float q[8];
+        if constexpr (MODE == kHalf) unpack8(o[j], q);
+        if constexpr (MODE == kShfl) {
+          if ((j * G + G) * 8 > r0) {
+            uint4 x;
+            x.x = __shfl_xor_sync(lane_grp, g[j].x, half >> 3);
+            x.y = __shfl_xor_sync(lane_grp, g[j].y, half >> 3);
+            x.z = __shfl_xor_sync(lane_grp, g[j].z, half >> 3);
+            x.w = __shfl_xor_sync(lane_grp, g[j].w, half >> 3);
+            unpack8(x, q);
+          }
         }
+        if (MODE != kNone && col >= r0 && col < p.D) rotate8<MODE>(f, q, cs + tt * half, col - r0, half, true);
       };
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int col = (j * G + gl) * 8;
-        if (col < p.norm) {
+        if (j * G * 8 < p.norm) {                // the same for every lane of the row
           float f[8], xf[8], w[8];
           rotated(j, col, f);
+          if (col >= p.norm) continue;
           unpack8(v[j], xf);
           load_w(s.w, col, w);
 #pragma unroll
@@ -298,18 +319,13 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(NrParams p) {
       __syncwarp(lane_grp);                       // every lane holds its columns: dx may be dy's buffer
       const float rho = rsqrtf(fmaf(ss, p.inv_norm, p.eps));
       const float c1 = rho * rho * rho * dot * p.inv_norm;
-      if (!on) continue;
       uint16_t* dx = s.dx + base;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int col = (j * G + gl) * 8;
-        if (col >= p.D) continue;
-        if (col >= p.norm && (MODE == kNone || col < r0)) {
-          *reinterpret_cast<uint4*>(dx + col) = g[j];
-          continue;
-        }
         float f[8];
         rotated(j, col, f);
+        if (!on || col >= p.D) continue;
         if (col < p.norm) {
           float xf[8], w[8];
           unpack8(v[j], xf);
@@ -375,8 +391,10 @@ __global__ void __launch_bounds__(256) norm_rope_dw_kernel(DwParams p) {
 
 // tokens per item, so that a block's rows fill its groups, and heads per
 // item: all of a token's heads when there are items enough for every SM four
-// times over, else as few as fill the block once (short decode batches)
-void plan_side(Side* s, int tokens, int rows_in_flight, int num_sms) {
+// times over, else as few as fill the block once (short decode batches).
+// Backward a block takes many items, and they are kept to four fillings, so
+// that the blocks' shares come out even.
+void plan_side(Side* s, int tokens, int rows_in_flight, int num_sms, bool back) {
   if (s->H == 0) {
     s->tile = 1;
     s->hc = 1;
@@ -388,21 +406,25 @@ void plan_side(Side* s, int tokens, int rows_in_flight, int num_sms) {
   if (s->tile > kTileTokens) s->tile = kTileTokens;
   const int tiles = (tokens + s->tile - 1) / s->tile;
   s->hc = tiles >= 4 * num_sms || s->H < rows_in_flight ? s->H : rows_in_flight;
+  if (back && s->hc > 4 * rows_in_flight) s->hc = 4 * rows_in_flight;
   s->hsplit = (s->H + s->hc - 1) / s->hc;
   s->items = tiles * s->hsplit;
 }
 
-// blocks of each side in the backward pass: about four per SM in all, shared
-// by rows, and a side with rows has at least one
-void plan_blocks(NrParams* p, int num_sms) {
+// blocks of each side in the backward pass: the resident ones shared by rows,
+// each side that has rows with at least one
+void plan_blocks(NrParams* p, int resident) {
   const long long q = p->side[0].H, k = p->side[1].H;
-  const long long total = 4ll * num_sms;
-  for (int i = 0; i < 2; ++i) {
-    Side& s = p->side[i];
-    long long n = s.H == 0 ? 0 : (total * s.H + q + k - 1) / (q + k);
+  for (Side& s : p->side) {
+    long long n = s.H == 0 ? 0 : resident * (long long)s.H / (q + k);
+    if (s.H > 0 && n < 1) n = 1;
     if (n > s.items) n = s.items;
     s.blocks = (int)n;
   }
+}
+int lanes_of(int D) { return D <= 64 ? 8 : D <= 640 ? 16 : 32; }
+int resident_blocks(int D, int num_sms) {
+  return num_sms * (D <= 256 ? bwd_blocks_per_sm<1>() : bwd_blocks_per_sm<4>());
 }
 
 template <int G, int V, int MODE>
@@ -418,17 +440,21 @@ cudaError_t launch_mode(const LaunchCtx& c, const NrParams& p, bool back) {
   note_launches(1);
   return cudaGetLastError();
 }
+// Half-split pairs lie r/2 columns apart: r/16 lanes when that is a power of
+// two below G and the rotated range starts on a multiple of r columns.
 template <int G, int V>
 cudaError_t launch_gv(const LaunchCtx& c, const NrParams& p, bool inter, bool back) {
   if (p.rope == 0) return launch_mode<G, V, kNone>(c, p, back);
-  return inter ? launch_mode<G, V, kInter>(c, p, back) : launch_mode<G, V, kHalf>(c, p, back);
+  if (inter) return launch_mode<G, V, kInter>(c, p, back);
+  const int lanes = p.rope / 16;
+  const bool shfl = (lanes & (lanes - 1)) == 0 && lanes < G && (p.D - p.rope) % p.rope == 0;
+  return shfl ? launch_mode<G, V, kShfl>(c, p, back) : launch_mode<G, V, kHalf>(c, p, back);
 }
-int lanes_of(int D) { return D <= 576 ? 8 : 32; }
 cudaError_t launch_nr(const LaunchCtx& c, const NrParams& p, bool inter, bool back) {
   if (p.D <= 64) return launch_gv<8, 1>(c, p, inter, back);
-  if (p.D <= 128) return launch_gv<8, 2>(c, p, inter, back);
-  if (p.D <= 256) return launch_gv<8, 4>(c, p, inter, back);
-  if (p.D <= 576) return launch_gv<8, 9>(c, p, inter, back);
+  if (p.D <= 128) return launch_gv<16, 1>(c, p, inter, back);
+  if (p.D <= 256) return launch_gv<16, 2>(c, p, inter, back);
+  if (p.D <= 640) return launch_gv<16, 5>(c, p, inter, back);
   return launch_gv<32, 4>(c, p, inter, back);
 }
 
@@ -451,7 +477,7 @@ dsa_status check_desc(const dsa_shape* s, const dsa_norm_rope_desc* d) {
   return DSA_OK;
 }
 
-NrParams make_params(const LaunchCtx& c, const dsa_shape* s, const dsa_norm_rope_desc* d) {
+NrParams make_params(const LaunchCtx& c, const dsa_shape* s, const dsa_norm_rope_desc* d, bool back) {
   NrParams p = {};
   p.map = api_kv_map(s);
   p.inv_freq = d->inv_freq;
@@ -467,7 +493,7 @@ NrParams make_params(const LaunchCtx& c, const dsa_shape* s, const dsa_norm_rope
   p.side[1].H = d->Hk;
   p.side[0].w = d->q_weight;
   p.side[1].w = d->k_weight;
-  for (Side& sd : p.side) plan_side(&sd, p.tokens, kThreads / lanes_of(d->D), c.num_sms);
+  for (Side& sd : p.side) plan_side(&sd, p.tokens, kThreads / lanes_of(d->D), c.num_sms, back);
   return p;
 }
 
@@ -482,9 +508,9 @@ using namespace dsa;
 
 extern "C" size_t dsa_norm_rope_workspace_size(const dsa_shape* s, const dsa_norm_rope_desc* d) {
   if (check_desc(s, d) != DSA_OK) return 0;
-  // at least one row of partial sums, at most four blocks per SM and side;
-  // sized for the largest SM count so that it does not depend on the device
-  return ((size_t)4 * 256 + 2) * (d->norm_cols > 0 ? d->norm_cols : 1) * sizeof(float);
+  // a row of partial sums for each resident block, one more for a side that
+  // would have had none; sized for 256 SMs, so that it depends on no device
+  return ((size_t)resident_blocks(d->D, 256) + 2) * (d->norm_cols > 0 ? d->norm_cols : 1) * sizeof(float);
 }
 
 extern "C" dsa_status dsa_norm_rope(const dsa_shape* s, const dsa_norm_rope_desc* d, const uint16_t* q,
@@ -494,7 +520,7 @@ extern "C" dsa_status dsa_norm_rope(const dsa_shape* s, const dsa_norm_rope_desc
   if (!rows_ok(d->Hq, q, q_out) || !rows_ok(d->Hk, k, k_out)) return DSA_ERR_INVALID_ARG;
   LaunchCtx c;
   if ((st = api_make_ctx(stream, &c)) != DSA_OK) return st;
-  NrParams p = make_params(c, s, d);
+  NrParams p = make_params(c, s, d, false);
   p.side[0].x = q;
   p.side[0].y = q_out;
   p.side[1].x = k;
@@ -513,8 +539,8 @@ extern "C" dsa_status dsa_norm_rope_backward(const dsa_shape* s, const dsa_norm_
   LaunchCtx c;
   if ((st = api_make_ctx(stream, &c)) != DSA_OK) return st;
   if (c.num_sms > 256) return DSA_ERR_UNSUPPORTED;
-  NrParams p = make_params(c, s, d);
-  plan_blocks(&p, c.num_sms);
+  NrParams p = make_params(c, s, d, true);
+  plan_blocks(&p, resident_blocks(d->D, c.num_sms));
   p.side[0].x = q;
   p.side[0].dy = dq_out;
   p.side[0].dx = dq;

@@ -191,8 +191,15 @@ def _p(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# the current stream's handle, without the Stream object that
+# torch.cuda.current_stream builds (3 us of a call's 12)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _need(t, dtype, name):
@@ -404,14 +411,32 @@ def forward(shape: Shape, inp: dict, out, lse, idx, ws, entry: str = "dsa_forwar
     return out, lse, idx
 
 
-def _need_here(t, dtype, name, numel=None):
-    """As _need, on the current device, with exactly numel elements where that is given."""
-    if (t.dtype != dtype or not t.is_contiguous() or t.get_device() < 0
-            or t.get_device() != torch.cuda.current_device()):
-        raise ValueError(f"{name}: need a contiguous tensor of {dtype} on the current CUDA device, got {t.dtype} "
-                         f"on {t.device} contiguous={t.is_contiguous()}")
-    if numel is not None and t.numel() != numel:
-        raise ValueError(f"{name}: need {numel} elements, got {t.numel()} ({tuple(t.shape)})")
+def _addresses(*specs):
+    """Addresses of tensors, each checked: specs are (tensor or None, dtype,
+    elements, name); contiguous, on the current device, of exactly that type
+    and size.  None (left out) has no address."""
+    dev = -1
+    out = []
+    for t, dtype, numel, name in specs:
+        if t is None:
+            out.append(None)
+            continue
+        if dev < 0:
+            dev = torch.cuda.current_device() if t.is_cuda else -2
+        if t.dtype is not dtype or t.numel() != numel or not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError(f"{name}: need a contiguous tensor of {numel} {dtype} on the current CUDA device, got "
+                             f"{tuple(t.shape)} {t.dtype} on {t.device} contiguous={t.is_contiguous()}")
+        out.append(t.data_ptr())
+    return out
+
+
+def _workspace(ws):
+    """Address and bytes of a workspace tensor (or None)."""
+    if ws is None:
+        return None, 0
+    if not ws.is_contiguous() or not ws.is_cuda or ws.get_device() != torch.cuda.current_device():
+        raise ValueError(f"workspace: need a contiguous tensor on the current CUDA device, got {ws.device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _pool_rows(shape: Shape) -> int:
@@ -423,12 +448,10 @@ def make_norm_rope(*, Hq: int, Hk: int, D: int, norm_cols: int, rope_cols: int, 
     """Description of dsa_norm_rope's rows.  q_weight, k_weight: float32 CUDA
     tensors [norm_cols] or None (ones); inv_freq: float32 CUDA tensor
     [rope_cols / 2], radians per position.  It keeps references to them."""
-    for t, n, name in ((q_weight, norm_cols, "q_weight"), (k_weight, norm_cols, "k_weight"),
-                       (inv_freq, rope_cols // 2, "inv_freq")):
-        if t is not None:
-            _need_here(t, torch.float32, name, n)
+    f32 = torch.float32
     d = NormRope(Hq, Hk, D, norm_cols, rope_cols, int(bool(interleaved)), eps,
-                 *(None if t is None else t.data_ptr() for t in (q_weight, k_weight, inv_freq)))
+                 *_addresses((q_weight, f32, norm_cols, "q_weight"), (k_weight, f32, norm_cols, "k_weight"),
+                             (inv_freq, f32, rope_cols // 2, "inv_freq")))
     d._keep = (q_weight, k_weight, inv_freq)
     return d
 
@@ -437,11 +460,9 @@ def norm_rope(shape: Shape, desc: NormRope, q, k, q_out, k_out):
     """RMS norm per head and rotation by position: q [B, T, Hq, D], k [B, T, Hk, D]
     bf16 -> q_out, k_out (a side with no heads is None; in place is allowed)."""
     n = shape.B * shape.T * desc.D
-    for t, H, name in ((q, desc.Hq, "q"), (q_out, desc.Hq, "q_out"), (k, desc.Hk, "k"), (k_out, desc.Hk, "k_out")):
-        if t is not None:
-            _need_here(t, torch.bfloat16, name, n * H)
-    _check("dsa_norm_rope", lib().dsa_norm_rope(
-        ctypes.byref(shape), ctypes.byref(desc), _p(q), _p(k), _p(q_out), _p(k_out), _stream()))
+    nq, nk, bf = n * desc.Hq, n * desc.Hk, torch.bfloat16
+    a = _addresses((q, bf, nq, "q"), (k, bf, nk, "k"), (q_out, bf, nq, "q_out"), (k_out, bf, nk, "k_out"))
+    _check("dsa_norm_rope", lib().dsa_norm_rope(ctypes.byref(shape), ctypes.byref(desc), *a, _stream()))
     return q_out, k_out
 
 
@@ -461,16 +482,12 @@ def norm_rope_backward(shape: Shape, desc: NormRope, q, k, dq_out, dk_out, dq, d
     """Gradients of norm_rope from its inputs and the gradients of its outputs;
     dq_weight, dk_weight float32 [norm_cols] are written (None: not wanted)."""
     n = shape.B * shape.T * desc.D
-    for t, H, name in ((q, desc.Hq, "q"), (dq_out, desc.Hq, "dq_out"), (dq, desc.Hq, "dq"),
-                       (k, desc.Hk, "k"), (dk_out, desc.Hk, "dk_out"), (dk, desc.Hk, "dk")):
-        if t is not None:
-            _need_here(t, torch.bfloat16, name, n * H)
-    for t, name in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
-        if t is not None:
-            _need_here(t, torch.float32, name, desc.norm_cols)
+    nq, nk, bf, f32 = n * desc.Hq, n * desc.Hk, torch.bfloat16, torch.float32
+    a = _addresses((q, bf, nq, "q"), (k, bf, nk, "k"), (dq_out, bf, nq, "dq_out"), (dk_out, bf, nk, "dk_out"),
+                   (dq, bf, nq, "dq"), (dk, bf, nk, "dk"), (dq_weight, f32, desc.norm_cols, "dq_weight"),
+                   (dk_weight, f32, desc.norm_cols, "dk_weight"))
     _check("dsa_norm_rope_backward", lib().dsa_norm_rope_backward(
-        ctypes.byref(shape), ctypes.byref(desc), _p(q), _p(k), _p(dq_out), _p(dk_out), _p(dq), _p(dk),
-        _p(dq_weight), _p(dk_weight), _p(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream()))
+        ctypes.byref(shape), ctypes.byref(desc), *a, *_workspace(ws), _stream()))
     return dq, dk
 
 
@@ -479,36 +496,24 @@ def cache_write(shape: Shape, *, kv=None, kv8=None, kv_scale=None, k_I=None, kI8
     """Quantise a step's new rows to e4m3 and write them to their places: kv
     [B, T, d_k] into the cache kv8, kv_scale; k_I [B, T, D_I] into kI8, kI_scale;
     q_I [B, T, H_I, D_I] into qI8, qI_scale.  Each part may be left out."""
-    n, rows = shape.B * shape.T, _pool_rows(shape)
-    for x, x8, sc, d, m, r, name in ((kv, kv8, kv_scale, shape.d_k, n, rows, "kv"),
-                                     (k_I, kI8, kI_scale, shape.D_I, n, rows, "k_I"),
-                                     (q_I, qI8, qI_scale, shape.D_I, n * shape.H_I, n * shape.H_I, "q_I")):
-        if x is not None:
-            _need_here(x, torch.bfloat16, name, m * d)
-        if x8 is not None:
-            _need_here(x8, torch.uint8, name + " bytes", r * d)
-        if sc is not None:
-            _need_here(sc, torch.float32, name + " scales", r)
-    _check("dsa_cache_write", lib().dsa_cache_write(
-        ctypes.byref(shape), _p(kv), _p(kv8), _p(kv_scale), _p(k_I), _p(kI8), _p(kI_scale), _p(q_I), _p(qI8),
-        _p(qI_scale), _stream()))
+    n, rows, d, D = shape.B * shape.T, _pool_rows(shape), shape.d_k, shape.D_I
+    nq = n * shape.H_I
+    bf, u8, f32 = torch.bfloat16, torch.uint8, torch.float32
+    a = _addresses((kv, bf, n * d, "kv"), (kv8, u8, rows * d, "kv8"), (kv_scale, f32, rows, "kv_scale"),
+                   (k_I, bf, n * D, "k_I"), (kI8, u8, rows * D, "kI8"), (kI_scale, f32, rows, "kI_scale"),
+                   (q_I, bf, nq * D, "q_I"), (qI8, u8, nq * D, "qI8"), (qI_scale, f32, nq, "qI_scale"))
+    _check("dsa_cache_write", lib().dsa_cache_write(ctypes.byref(shape), *a, _stream()))
 
 
 def cache_read(shape: Shape, s_begin: int, s_count: int, *, kv8=None, kv_scale=None, kv=None, kI8=None,
                kI_scale=None, k_I=None) -> None:
     """Tokens [s_begin, s_begin + s_count) of every sequence back as bf16 rows:
     kv [B, s_count, d_k], k_I [B, s_count, D_I].  Each part may be left out."""
-    n, rows = shape.B * s_count, _pool_rows(shape)
-    for x, x8, sc, d, name in ((kv, kv8, kv_scale, shape.d_k, "kv"), (k_I, kI8, kI_scale, shape.D_I, "k_I")):
-        if x is not None:
-            _need_here(x, torch.bfloat16, name, n * d)
-        if x8 is not None:
-            _need_here(x8, torch.uint8, name + " bytes", rows * d)
-        if sc is not None:
-            _need_here(sc, torch.float32, name + " scales", rows)
-    _check("dsa_cache_read", lib().dsa_cache_read(
-        ctypes.byref(shape), s_begin, s_count, _p(kv8), _p(kv_scale), _p(kv), _p(kI8), _p(kI_scale), _p(k_I),
-        _stream()))
+    n, rows, d, D = shape.B * s_count, _pool_rows(shape), shape.d_k, shape.D_I
+    bf, u8, f32 = torch.bfloat16, torch.uint8, torch.float32
+    a = _addresses((kv8, u8, rows * d, "kv8"), (kv_scale, f32, rows, "kv_scale"), (kv, bf, n * d, "kv"),
+                   (kI8, u8, rows * D, "kI8"), (kI_scale, f32, rows, "kI_scale"), (k_I, bf, n * D, "k_I"))
+    _check("dsa_cache_read", lib().dsa_cache_read(ctypes.byref(shape), s_begin, s_count, *a, _stream()))
 
 
 def workspace8_size(shape: Shape) -> int:
@@ -523,48 +528,37 @@ def alloc_workspace8(shape: Shape) -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device="cuda")
 
 
-def _need_attn8(shape, q, kv8, kv_scale, out, lse):
-    n, rows = shape.B * shape.T * shape.H, _pool_rows(shape)
-    _need_here(q, torch.bfloat16, "q", n * shape.d_k)
-    _need_here(kv8, torch.uint8, "kv8", rows * shape.d_k)
-    _need_here(kv_scale, torch.float32, "kv_scale", rows)
-    _need_here(out, torch.bfloat16, "out", n * shape.d_v)
-    if lse is not None:
-        _need_here(lse, torch.float32, "lse", n)
-
-
 def sparse_attn8(shape: Shape, q, kv8, kv_scale, idx, out, lse=None, ws=None):
     """Step C over an 8-bit cache (e4m3 rows kv8, float32 scales kv_scale)."""
-    _need_attn8(shape, q, kv8, kv_scale, out, lse)
-    _need_here(idx, torch.int32, "idx", shape.B * shape.T * shape.k)
-    _check("dsa_sparse_attn8", lib().dsa_sparse_attn8(
-        ctypes.byref(shape), _p(q), _p(kv8), _p(kv_scale), _p(idx), _p(out), _p(lse), _p(ws),
-        0 if ws is None else ws.numel() * ws.element_size(), _stream()))
+    t, rows = shape.B * shape.T, _pool_rows(shape)
+    n, bf = t * shape.H, torch.bfloat16
+    a = _addresses((q, bf, n * shape.d_k, "q"), (kv8, torch.uint8, rows * shape.d_k, "kv8"),
+                   (kv_scale, torch.float32, rows, "kv_scale"), (idx, torch.int32, t * shape.k, "idx"),
+                   (out, bf, n * shape.d_v, "out"), (lse, torch.float32, n, "lse"))
+    _check("dsa_sparse_attn8", lib().dsa_sparse_attn8(ctypes.byref(shape), *a, *_workspace(ws), _stream()))
     return out, lse
 
 
 def dense_attn8(shape: Shape, q, kv8, kv_scale, out, lse=None, ws=None):
     """Dense causal attention over an 8-bit cache (no selection)."""
-    _need_attn8(shape, q, kv8, kv_scale, out, lse)
-    _check("dsa_dense_attn8", lib().dsa_dense_attn8(
-        ctypes.byref(shape), _p(q), _p(kv8), _p(kv_scale), _p(out), _p(lse), _p(ws),
-        0 if ws is None else ws.numel() * ws.element_size(), _stream()))
+    n, rows, bf = shape.B * shape.T * shape.H, _pool_rows(shape), torch.bfloat16
+    a = _addresses((q, bf, n * shape.d_k, "q"), (kv8, torch.uint8, rows * shape.d_k, "kv8"),
+                   (kv_scale, torch.float32, rows, "kv_scale"), (out, bf, n * shape.d_v, "out"),
+                   (lse, torch.float32, n, "lse"))
+    _check("dsa_dense_attn8", lib().dsa_dense_attn8(ctypes.byref(shape), *a, *_workspace(ws), _stream()))
     return out, lse
 
 
 def forward8(shape: Shape, inp: dict, out, lse, idx, ws):
     """The whole path over an 8-bit cache through dsa_forward8."""
-    n, rows = shape.B * shape.T, _pool_rows(shape)
-    for t, d, m in (("q_I", torch.uint8, n * shape.H_I * shape.D_I), ("q_scale", torch.float32, n * shape.H_I),
-                    ("w", torch.float32, n * shape.H_I), ("k_I", torch.uint8, rows * shape.D_I),
-                    ("k_scale", torch.float32, rows)):
-        _need_here(inp[t], d, t, m)
-    _need_attn8(shape, inp["q"], inp["kv8"], inp["kv_scale"], out, lse)
-    _need_here(idx, torch.int32, "idx", n * shape.k)
-    ins = Inputs8(*(inp[t].data_ptr() for t in INPUT8_NAMES))
+    t, rows, u8, f32, bf = shape.B * shape.T, _pool_rows(shape), torch.uint8, torch.float32, torch.bfloat16
+    h, n = t * shape.H_I, t * shape.H
+    sizes = dict(q_I=(u8, h * shape.D_I), q_scale=(f32, h), w=(f32, h), k_I=(u8, rows * shape.D_I),
+                 k_scale=(f32, rows), q=(bf, n * shape.d_k), kv8=(u8, rows * shape.d_k), kv_scale=(f32, rows))
+    ins = Inputs8(*_addresses(*((inp[m], *sizes[m], m) for m in INPUT8_NAMES)))
+    a = _addresses((out, bf, n * shape.d_v, "out"), (lse, f32, n, "lse"), (idx, torch.int32, t * shape.k, "idx"))
     _check("dsa_forward8", lib().dsa_forward8(
-        ctypes.byref(shape), ctypes.byref(ins), _p(out), _p(lse), _p(idx), _p(ws),
-        0 if ws is None else ws.numel() * ws.element_size(), _stream()))
+        ctypes.byref(shape), ctypes.byref(ins), *a, *_workspace(ws), _stream()))
     return out, lse, idx
 
 
