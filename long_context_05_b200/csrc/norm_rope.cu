@@ -10,18 +10,20 @@
 //   dx_c = rho (w_c g_c - x_c rho^2 mean_{c < n}(w g x)),  dw_c = sum over rows of g_c x_c rho.
 //
 // Nothing is reused between rows but the angles of a token and the weights,
-// so the bound is HBM: 4 bytes per element forward, 6 backward.  A row is
-// held in the registers of G lanes (16 up to 640 columns: a 16-byte load of
-// each covers 256 contiguous bytes of a row), read once, reduced by shuffles
-// and written once.  The pair of a rotated column comes from another lane by
-// shuffles where it lies in the same step of 16 G bytes, else it is read again
-// (from L1).  The r/2 sines and cosines of a token are
-// formed once per block, in shared memory, for all heads the block handles.
+// so the bound is HBM: 4 bytes per element forward, 6 backward.  All rows of
+// a side lie one behind the other, so a tile of them is one contiguous piece
+// of memory whatever its heads and tokens.  Every warp works by itself: it
+// takes a run of tiles of about 4.5 KB and keeps kStages of them on their way
+// into shared memory of its own by bulk copies, so no registers hold loads in
+// flight and no warp waits for another.  A row is worked on by G lanes (16 up
+// to 640 columns; U rows of each group at a time where rows are short, for
+// independent work), reduced by shuffles and written once by 16-byte stores.
+// The r/2 sines and cosines of a token are formed once per warp and token.
 // The angle is reduced in FP64 (pos times f is exact to 2^-53 there; FP32
 // would be off by 2^-24 of the whole angle, half a degree at position 128K),
 // then sincospif of the fraction of a turn.
 //
-// The weight gradients stay in FP32 registers over a block's rows (a lane
+// The weight gradients stay in FP32 registers over a warp's rows (a lane
 // meets the same columns in every row), are added in a fixed order over the
 // block and then over the blocks: the same call gives the same bits.
 #include "internal.h"
@@ -30,14 +32,18 @@
 namespace dsa {
 namespace {
 
+using namespace sm100;
+
 constexpr int kThreads = 128;
-constexpr int kTileTokens = 16;   // tokens whose angles a block holds at a time, at most
-constexpr int kMaxHalf = 128;     // rotated pairs, at most (r <= 256)
+constexpr int kWarps = kThreads / 32;
+constexpr int kStages = 2;
+constexpr int kTileBytes = 4608;    // a warp's tile (both tensors in the backward pass), at most
+constexpr int kMaxTileRows = 32;
+constexpr int kMaxHalf = 128;       // rotated pairs, at most (r <= 256)
 constexpr int kMaxD = 1024;
 
-// kHalf: pairs (i, i + r/2), the partner read again; kShfl: the same with the
-// partner columns in lane ^ (r / 16) of the same step; kInter: pairs (2i, 2i + 1)
-enum RopeMode { kNone = 0, kHalf = 1, kInter = 2, kShfl = 3 };
+// kHalf: pairs (i, i + r/2); kInter: pairs (2i, 2i + 1)
+enum RopeMode { kNone = 0, kHalf = 1, kInter = 2 };
 
 struct Side {
   const uint16_t* x;     // rows in [tokens, H, D]
@@ -47,49 +53,92 @@ struct Side {
   const float* w;        // [norm_cols] or null (ones)
   float* dw_part;        // backward: [blocks of this side, norm_cols] partial sums
   int H;
-  int tile;              // tokens of an item
-  int hc;                // heads of an item
-  int items;             // work items of this side
-  int hsplit;            // items per token tile
-  int blocks;            // backward: blocks of this side
+  int rows;              // tokens * H
+  int tiles;
+  int blocks;            // blocks that share the tiles
+  float inv_H;
 };
 
 struct NrParams {
   Side side[2];
   KvMap map;
   const float* inv_freq;
-  int tokens, T, D, norm, rope;
+  int T, D, norm, rope;
+  int rt;                // rows of a tile
+  int tensor_bytes;      // one tensor's tile in shared memory
+  int warp_bytes;        // a warp's stages and angles
   float inv_norm, eps;
+  long long wait_ns;
   DevErr* err;
 };
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+// Eight columns as four pairs, for the packed FP32 instructions: half the
+// instructions of the scalar ones, and the forward kernel is bound by issue
+// as much as by HBM.
+struct F8 {
+  uint64_t v[4];
+};
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F8 unpack8(const uint4& v) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  F8 f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f.v[i] = pair(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+  return f;
+}
+__device__ __forceinline__ uint4 pack8(const F8& f) {
+  uint32_t u[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(u[i] << 16);
-    f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    const float2 x = unpair(f.v[i]);
+    u[i] = pack_bf16x2(x.x, x.y);
   }
+  return make_uint4(u[0], u[1], u[2], u[3]);
 }
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(sm100::pack_bf16x2(f[0], f[1]), sm100::pack_bf16x2(f[2], f[3]), sm100::pack_bf16x2(f[4], f[5]),
-                    sm100::pack_bf16x2(f[6], f[7]));
-}
-__device__ __forceinline__ void load_w(const float* w, int col, float (&f)[8]) {
+__device__ __forceinline__ F8 load_w(const float* w, int col) {
+  F8 f;
   if (w == nullptr) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = 1.f;
-    return;
+    for (int i = 0; i < 4; ++i) f.v[i] = pair(1.f, 1.f);
+    return f;
   }
-  const float4 a = __ldg(reinterpret_cast<const float4*>(w + col)), b = __ldg(reinterpret_cast<const float4*>(w + col) + 1);
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2*>(w + col));
+  const ulonglong2 b = __ldg(reinterpret_cast<const ulonglong2*>(w + col) + 1);
+  f.v[0] = a.x; f.v[1] = a.y; f.v[2] = b.x; f.v[3] = b.y;
+  return f;
 }
 
-// cos and sin of the angles of tokens [n0, n0 + nt): cs[tt * half + i]
+// contiguous copy of `bytes` (a multiple of 16) from global to shared memory
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// cos and sin of the angles of tokens [n0, n0 + nt): cs[tt * half + i] (one warp)
 __device__ __forceinline__ void fill_angles(const NrParams& p, float2* cs, int n0, int nt) {
   const int half = p.rope >> 1;
-  for (int e = threadIdx.x; e < nt * half; e += kThreads) {
+  for (int e = threadIdx.x & 31; e < nt * half; e += 32) {
     const int tt = e / half, i = e - tt * half;
     const int n = n0 + tt, b = n / p.T, t = n - b * p.T;
     const int pos = p.map.len(b, i == 0 ? p.err : nullptr, ERR_SITE_NORM) - p.T + t;
@@ -101,266 +150,268 @@ __device__ __forceinline__ void fill_angles(const NrParams& p, float2* cs, int n
   }
 }
 
-// Rotate the eight columns at `col` (offset rc = col - (D - r) >= 0 into the
-// rotated range).  kHalf, kShfl: o holds the partner columns rc +- r/2.  back: by
-// the opposite angle.
+// Rotate the eight columns rc .. rc + 7 of the rotated range.  kHalf: o holds
+// the partner columns rc +- r/2.  back: by the opposite angle.
 template <int MODE>
-__device__ __forceinline__ void rotate8(float (&z)[8], const float (&o)[8], const float2* cs, int rc, int half,
-                                        bool back) {
+__device__ __forceinline__ void rotate8(F8& z, const F8& o, const float2* cs, int rc, int half, bool back) {
   if constexpr (MODE == kInter) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 a = cs[(rc >> 1) + i];
+      const float2 a = cs[(rc >> 1) + i], z2 = unpair(z.v[i]);
       const float s = back ? -a.y : a.y;
-      const float u = z[2 * i], v = z[2 * i + 1];
-      z[2 * i] = u * a.x - v * s;
-      z[2 * i + 1] = u * s + v * a.x;
+      z.v[i] = pair(z2.x * a.x - z2.y * s, z2.x * s + z2.y * a.x);
     }
-  } else if constexpr (MODE == kHalf || MODE == kShfl) {
+  } else if constexpr (MODE == kHalf) {
     const bool first = rc < half;
-    const float2* a0 = cs + (first ? rc : rc - half);
+    const float4* a0 = reinterpret_cast<const float4*>(cs + (first ? rc : rc - half));
+    const float sign = first == back ? 1.f : -1.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 a = a0[i];
-      float s = back ? -a.y : a.y;
-      if (first) s = -s;
-      z[i] = fmaf(o[i], s, z[i] * a.x);
+    for (int i = 0; i < 4; ++i) {
+      const float4 a = a0[i];                     // two angles
+      z.v[i] = fma2(o.v[i], pair(a.y * sign, a.w * sign), mul2(z.v[i], pair(a.x, a.z)));
     }
   }
 }
 
-// which side and item this block works on: the q side's items come first
-__device__ __forceinline__ void item_of(const Side& s, int tokens, int item, int& n0, int& nt, int& h0, int& hn) {
-  const int tile = item / s.hsplit, hs = item - tile * s.hsplit;
-  n0 = tile * s.tile;
-  nt = min(s.tile, tokens - n0);
-  h0 = hs * s.hc;
-  hn = min(s.hc, s.H - h0);
-}
+// Blocks of an SM that the registers leave room for.
+constexpr int blocks_per_sm(int V, bool back) { return V >= 4 ? (back ? 3 : 5) : (back ? 5 : 6); }
 
-template <int G, int V, int MODE>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(NrParams p) {
-  extern __shared__ float2 cs[];
-  constexpr int kRows = kThreads / G;             // rows in flight in the block
-  const int gl = threadIdx.x % G, grp = threadIdx.x / G;
-  int item = blockIdx.x;
-  const int sd = item < p.side[0].items ? 0 : 1;
-  if (sd) item -= p.side[0].items;
-  const Side& s = p.side[sd];
-  int n0, nt, h0, hn;
-  item_of(s, p.tokens, item, n0, nt, h0, hn);
-  if (MODE != kNone) {
-    fill_angles(p, cs, n0, nt);
-    __syncthreads();
-  }
-  const int half = p.rope >> 1, r0 = p.D - p.rope;
-  const int nrows = nt * hn;
-  const unsigned lane_grp = G == 32 ? 0xffffffffu : ((1u << (G & 31)) - 1u) << ((threadIdx.x & 31) / G * G);
-  for (int rr = 0; rr < nrows; rr += kRows) {
-    const bool on = rr + grp < nrows;
-    const int r = on ? rr + grp : rr;             // idle groups read and write nothing
-    const int tt = r / hn, h = h0 + r - tt * hn;
-    const size_t base = ((size_t)(n0 + tt) * s.H + h) * p.D;
-    const uint16_t* x = s.x + base;
-    uint4 v[V], o[MODE == kHalf ? V : 1];
-    float ss = 0.f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int col = (j * G + gl) * 8;
-      v[j] = make_uint4(0u, 0u, 0u, 0u);
-      if (on && col < p.D) v[j] = *reinterpret_cast<const uint4*>(x + col);
-      if constexpr (MODE == kHalf) {
-        // the partner columns, read (from L1) before any lane writes the row
-        if (on && col < p.D && col >= r0) o[j] = *reinterpret_cast<const uint4*>(x + (col - r0 < half ? col + half : col - half));
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      if ((j * G + gl) * 8 < p.norm) {
-        float f[8];
-        unpack8(v[j], f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
-      }
-    }
-#pragma unroll
-    for (int d = 1; d < G; d <<= 1) ss += __shfl_xor_sync(lane_grp, ss, d);
-    __syncwarp(lane_grp);                         // every lane holds its columns: the row may be written over
-    const float rho = rsqrtf(fmaf(ss, p.inv_norm, p.eps));
-    uint16_t* y = s.y + base;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int col = (j * G + gl) * 8;
-      float f[8], g[8];
-      unpack8(v[j], f);
-      if (col < p.norm) {
-        float w[8];
-        load_w(s.w, col, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= rho * w[i];
-      }
-      if constexpr (MODE == kShfl) {
-        // every lane of the row takes part in a step that holds rotated columns
-        if ((j * G + G) * 8 > r0) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) g[i] = __shfl_xor_sync(lane_grp, f[i], half >> 3);
-        }
-      }
-      if (!on || col >= p.D) continue;
-      if (MODE != kNone && col >= r0) {
-        if constexpr (MODE == kHalf) {
-          const int pc = col - r0 < half ? col + half : col - half;
-          unpack8(o[j], g);
-          if (pc < p.norm) {
-            float w[8];
-            load_w(s.w, pc, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] *= rho * w[i];
-          }
-        }
-        rotate8<MODE>(f, g, cs + tt * half, col - r0, half, false);
-      } else if (p.norm <= col) {
-        *reinterpret_cast<uint4*>(y + col) = v[j];
-        continue;
-      }
-      *reinterpret_cast<uint4*>(y + col) = pack8(f);
-    }
-  }
-}
-
-// Backward.  A block keeps to one side and takes its items in turn; the grid
-// is what is resident at once, so that every block has an equal share.
-template <int V>
-constexpr int bwd_blocks_per_sm() { return V >= 4 ? 3 : 6; }
-template <int G, int V, int MODE>
-__global__ void __launch_bounds__(kThreads, bwd_blocks_per_sm<V>()) norm_rope_bwd_kernel(NrParams p) {
-  extern __shared__ float2 cs[];
-  constexpr int kRows = kThreads / G;
-  const int gl = threadIdx.x % G, grp = threadIdx.x / G;
+template <int G, int V, int MODE, bool BACK>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(V, BACK)) norm_rope_kernel(NrParams p) {
+  extern __shared__ uint4 smem4[];
+  __shared__ uint64_t full_bar[kWarps][kStages];
+  constexpr int GP = 32 / G;                      // groups of a warp
+  constexpr int U = V == 1 ? (BACK ? 2 : 4) : V == 2 ? 2 : 1;
+  constexpr bool HOIST = V <= 2;                  // weights stay in registers
+  constexpr int kTensors = BACK ? 2 : 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gl = lane % G, grp = lane / G;
   const int sd = (int)blockIdx.x < p.side[0].blocks ? 0 : 1;
   const int blk = blockIdx.x - (sd ? p.side[0].blocks : 0);
   const Side& s = p.side[sd];
   const int half = p.rope >> 1, r0 = p.D - p.rope;
-  const unsigned lane_grp = G == 32 ? 0xffffffffu : ((1u << (G & 31)) - 1u) << ((threadIdx.x & 31) / G * G);
-  float acc[V][8];
+  const unsigned lane_grp = G == 32 ? 0xffffffffu : ((1u << (G & 31)) - 1u) << (grp * G);
+  uint8_t* ring = reinterpret_cast<uint8_t*>(smem4) + warp * p.warp_bytes;
+  float2* cs = reinterpret_cast<float2*>(ring + kStages * kTensors * p.tensor_bytes);
+  uint64_t* full = full_bar[warp];
+  const int workers = s.blocks * kWarps, me = blk * kWarps + warp;
+  const int tile0 = (int)((long long)s.tiles * me / workers), tile1 = (int)((long long)s.tiles * (me + 1) / workers);
+  const bool need_x = !BACK || p.norm > 0;
+  auto load_tile = [&](int tile) {
+    const int st = (tile - tile0) % kStages;
+    const uint32_t bytes = (uint32_t)min(p.rt, s.rows - tile * p.rt) * p.D * 2;
+    const size_t at = (size_t)tile * p.rt * p.D;
+    mbar_arrive_expect_tx(&full[st], bytes * (BACK && need_x ? 2 : 1));
+    uint8_t* d = ring + st * kTensors * p.tensor_bytes;
+    bulk_load(d, (BACK ? s.dy : s.x) + at, bytes, &full[st]);
+    if (BACK && need_x) bulk_load(d + p.tensor_bytes, s.x + at, bytes, &full[st]);
+  };
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init();
+    for (int i = tile0; i < tile1 && i < tile0 + kStages; ++i) load_tile(i);
+  }
+  __syncwarp();
+  F8 wr[HOIST ? V : 1];
+  if constexpr (HOIST) {
 #pragma unroll
-  for (int j = 0; j < V; ++j)
+    for (int j = 0; j < V; ++j)
+      if ((j * G + gl) * 8 < p.norm) wr[j] = load_w(s.w, (j * G + gl) * 8);
+  }
+  auto weights = [&](int j, int col) -> F8 {
+    if constexpr (HOIST) return wr[j];
+    else return load_w(s.w, col);
+  };
+  F8 acc[BACK ? V : 1];
+  if constexpr (BACK) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[j][i] = 0.f;
-  for (int item = blk; item < s.items; item += s.blocks) {
-    int n0, nt, h0, hn;
-    item_of(s, p.tokens, item, n0, nt, h0, hn);
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j].v[i] = 0ull;
+  }
+  const AbortSources no_abort{nullptr, nullptr};
+  int n_lo = 0, n_cnt = 0;                        // tokens whose angles cs holds
+  bool ok = true;
+  for (int tile = tile0; tile < tile1; ++tile) {
+    const int st = (tile - tile0) % kStages;
+    const int row0 = tile * p.rt, nr = min(p.rt, s.rows - row0);
+    const int n0 = row0 / s.H, off = row0 - n0 * s.H;
     if (MODE != kNone) {
-      __syncthreads();                            // the last item's angles are no longer read
-      fill_angles(p, cs, n0, nt);
-      __syncthreads();
+      const int nt = (off + nr - 1) / s.H + 1;
+      if (n0 < n_lo || n0 + nt > n_lo + n_cnt) {
+        fill_angles(p, cs, n0, nt);
+        n_lo = n0;
+        n_cnt = nt;
+        __syncwarp();
+      }
     }
-    const int nrows = nt * hn;
-    for (int rr = 0; rr < nrows; rr += kRows) {
-      const bool on = rr + grp < nrows;
-      const int r = on ? rr + grp : rr;
-      const int tt = r / hn, h = h0 + r - tt * hn;
-      const size_t base = ((size_t)(n0 + tt) * s.H + h) * p.D;
-      uint4 v[V], g[V], o[MODE == kHalf ? V : 1];
+    if (ok && !mbar_wait(&full[st], (uint32_t)((tile - tile0) / kStages) & 1, p.wait_ns, no_abort)) {
+      report_error(p.err, DSA_ERR_TIMEOUT, ERR_SITE_NORM | (2u << 8));
+      ok = false;
+    }
+    const uint8_t* sA = ring + st * kTensors * p.tensor_bytes;     // x forward, dy backward
+    for (int rr = 0; rr < nr; rr += GP * U) {
+      int r[U];
+      uint4 v[U][V];
+      uint64_t ss2[U], dot2[U];
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int col = (j * G + gl) * 8;
-        v[j] = make_uint4(0u, 0u, 0u, 0u);
-        g[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (on && col < p.D) {
-          g[j] = *reinterpret_cast<const uint4*>(s.dy + base + col);
-          if (col < p.norm) v[j] = *reinterpret_cast<const uint4*>(s.x + base + col);
-          if constexpr (MODE == kHalf) {
-            if (col >= r0)
-              o[j] = *reinterpret_cast<const uint4*>(s.dy + base + (col - r0 < half ? col + half : col - half));
-          }
+      for (int u = 0; u < U; ++u) {
+        r[u] = min(rr + u * GP + grp, nr - 1);    // groups past the tile follow its last row and write nothing
+        ss2[u] = dot2[u] = 0ull;
+        const uint4* ra = reinterpret_cast<const uint4*>(sA + r[u] * p.D * 2);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const int col = (j * G + gl) * 8;
+          v[u][j] = make_uint4(0u, 0u, 0u, 0u);
+          if (col < p.D) v[u][j] = ra[col >> 3];
         }
       }
-      // g = R^T dy, kept in FP32 where it was rotated and also normalised;
-      // ss = sum x^2, dot = sum w g x
-      float ss = 0.f, dot = 0.f;
-      auto rotated = [&](int j, int col, float (&f)[8]) {
-        unpack8(g[j], f);
-        float q[8];
-        if constexpr (MODE == kHalf) unpack8(o[j], q);
-        if constexpr (MODE == kShfl) {
-          if ((j * G + G) * 8 > r0) {
-            uint4 x;
-            x.x = __shfl_xor_sync(lane_grp, g[j].x, half >> 3);
-            x.y = __shfl_xor_sync(lane_grp, g[j].y, half >> 3);
-            x.z = __shfl_xor_sync(lane_grp, g[j].z, half >> 3);
-            x.w = __shfl_xor_sync(lane_grp, g[j].w, half >> 3);
-            unpack8(x, q);
-          }
+      // the angles of row r: its token within those of cs ((off + r) / H by
+      // the reciprocal: both below 2^11, exact with the half)
+      auto angles = [&](int r_) -> const float2* {
+        return cs + (n0 - n_lo + (int)(((float)(off + r_) + 0.5f) * s.inv_H)) * half;
+      };
+      auto partner = [&](int u, int col) -> F8 {
+        const int pc = col - r0 < half ? col + half : col - half;
+        return unpack8(*reinterpret_cast<const uint4*>(sA + r[u] * p.D * 2 + pc * 2));
+      };
+      // backward: g = R^T dy at this lane's columns of step j
+      auto rotated = [&](int u, int j, int col) -> F8 {
+        F8 f = unpack8(v[u][j]);
+        if (MODE != kNone && col >= r0) {
+          F8 q = f;
+          if constexpr (MODE == kHalf) q = partner(u, col);
+          rotate8<MODE>(f, q, angles(r[u]), col - r0, half, true);
         }
-        if (MODE != kNone && col >= r0 && col < p.D) rotate8<MODE>(f, q, cs + tt * half, col - r0, half, true);
+        return f;
+      };
+      auto x_of = [&](int u, int col) -> F8 {
+        return unpack8(*reinterpret_cast<const uint4*>(sA + p.tensor_bytes + r[u] * p.D * 2 + col * 2));
       };
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int col = (j * G + gl) * 8;
-        if (j * G * 8 < p.norm) {                // the same for every lane of the row
-          float f[8], xf[8], w[8];
-          rotated(j, col, f);
-          if (col >= p.norm) continue;
-          unpack8(v[j], xf);
-          load_w(s.w, col, w);
+        if (col < p.norm) {
+          if constexpr (!BACK) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            ss = fmaf(xf[i], xf[i], ss);
-            dot = fmaf(f[i] * xf[i], w[i], dot);
+            for (int u = 0; u < U; ++u) {
+              const F8 f = unpack8(v[u][j]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) ss2[u] = fma2(f.v[i], f.v[i], ss2[u]);
+            }
+          } else {
+            const F8 w = weights(j, col);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const F8 f = rotated(u, j, col), x = x_of(u, col);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                ss2[u] = fma2(x.v[i], x.v[i], ss2[u]);
+                dot2[u] = fma2(mul2(f.v[i], x.v[i]), w.v[i], dot2[u]);
+              }
+            }
           }
         }
       }
+      float ss[U], dot[U];
 #pragma unroll
-      for (int d = 1; d < G; d <<= 1) {
-        ss += __shfl_xor_sync(lane_grp, ss, d);
-        dot += __shfl_xor_sync(lane_grp, dot, d);
+      for (int u = 0; u < U; ++u) {
+        const float2 a = unpair(ss2[u]), d = unpair(dot2[u]);
+        ss[u] = a.x + a.y;
+        dot[u] = d.x + d.y;
       }
-      __syncwarp(lane_grp);                       // every lane holds its columns: dx may be dy's buffer
-      const float rho = rsqrtf(fmaf(ss, p.inv_norm, p.eps));
-      const float c1 = rho * rho * rho * dot * p.inv_norm;
-      uint16_t* dx = s.dx + base;
+#pragma unroll
+      for (int d = 1; d < G; d <<= 1)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          ss[u] += __shfl_xor_sync(lane_grp, ss[u], d);
+          if (BACK) dot[u] += __shfl_xor_sync(lane_grp, dot[u], d);
+        }
+      uint64_t rho[U], c1[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float h = rsqrtf(fmaf(ss[u], p.inv_norm, p.eps));
+        const float c = -(h * h * h * dot[u] * p.inv_norm);
+        rho[u] = pair(h, h);
+        c1[u] = pair(c, c);
+      }
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int col = (j * G + gl) * 8;
-        float f[8];
-        rotated(j, col, f);
-        if (!on || col >= p.D) continue;
-        if (col < p.norm) {
-          float xf[8], w[8];
-          unpack8(v[j], xf);
-          load_w(s.w, col, w);
+        if (col >= p.D) continue;
+        const bool rot = MODE != kNone && col >= r0, nrm = col < p.norm;
+        F8 w = {};
+        if (nrm) w = weights(j, col);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            acc[j][i] = fmaf(f[i] * rho, xf[i], acc[j][i]);
-            f[i] = fmaf(rho * w[i], f[i], -c1 * xf[i]);
+        for (int u = 0; u < U; ++u) {
+          if (!ok || rr + u * GP + grp >= nr) continue;
+          uint4* dst = reinterpret_cast<uint4*>((BACK ? s.dx : s.y) + (size_t)(row0 + r[u]) * p.D + col);
+          if (!nrm && !rot) {
+            *dst = v[u][j];
+            continue;
           }
+          F8 f;
+          if constexpr (!BACK) {
+            f = unpack8(v[u][j]);
+            if (nrm) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) f.v[i] = mul2(mul2(f.v[i], rho[u]), w.v[i]);
+            }
+            if (rot) {
+              F8 g = f;
+              if constexpr (MODE == kHalf) {
+                const int pc = col - r0 < half ? col + half : col - half;
+                g = partner(u, col);
+                if (pc < p.norm) {
+                  const F8 wp = load_w(s.w, pc);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) g.v[i] = mul2(mul2(g.v[i], rho[u]), wp.v[i]);
+                }
+              }
+              rotate8<MODE>(f, g, angles(r[u]), col - r0, half, false);
+            }
+          } else {
+            f = rotated(u, j, col);
+            if (nrm) {
+              const F8 x = x_of(u, col);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint64_t gr = mul2(f.v[i], rho[u]);
+                acc[j].v[i] = fma2(gr, x.v[i], acc[j].v[i]);
+                f.v[i] = fma2(gr, w.v[i], mul2(c1[u], x.v[i]));
+              }
+            }
+          }
+          *dst = pack8(f);
         }
-        *reinterpret_cast<uint4*>(dx + col) = pack8(f);
       }
     }
+    __syncwarp();                                 // the stage is read
+    if (lane == 0 && ok && tile + kStages < tile1) load_tile(tile + kStages);
   }
-  if (s.dw_part == nullptr) return;
-  // the groups' sums, in group order: first over the groups of a warp by
-  // shuffles, then over the warps through shared memory
-  __syncthreads();
-  float* red = reinterpret_cast<float*>(cs);      // [kThreads / 32][G * V * 8]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if constexpr (BACK) {
+    if (s.dw_part == nullptr) return;
+    // the groups' sums, in group order: first over the groups of a warp by
+    // shuffles, then over the warps through shared memory (every tile has landed)
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(smem4);  // [kWarps][G * V * 8]
 #pragma unroll
-  for (int j = 0; j < V; ++j)
+    for (int j = 0; j < V; ++j)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float a = acc[j][i];
+      for (int i = 0; i < 8; ++i) {
+        const float2 two = unpair(acc[j].v[i / 2]);
+        float a = i & 1 ? two.y : two.x;
 #pragma unroll
-      for (int d = G; d < 32; d <<= 1) a += __shfl_xor_sync(0xffffffffu, a, d);
-      if (lane < G) red[warp * (G * V * 8) + (j * G + gl) * 8 + i] = a;
+        for (int d = G; d < 32; d <<= 1) a += __shfl_xor_sync(0xffffffffu, a, d);
+        if (lane < G) red[warp * (G * V * 8) + (j * G + gl) * 8 + i] = a;
+      }
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.norm; c += kThreads) {
+      float a = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) a += red[w * (G * V * 8) + c];
+      s.dw_part[(size_t)blk * p.norm + c] = a;
     }
-  __syncthreads();
-  for (int c = threadIdx.x; c < p.norm; c += kThreads) {
-    float a = 0.f;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) a += red[w * (G * V * 8) + c];
-    s.dw_part[(size_t)blk * p.norm + c] = a;
   }
 }
 
@@ -389,73 +440,88 @@ __global__ void __launch_bounds__(256) norm_rope_dw_kernel(DwParams p) {
   }
 }
 
-// tokens per item, so that a block's rows fill its groups, and heads per
-// item: all of a token's heads when there are items enough for every SM four
-// times over, else as few as fill the block once (short decode batches).
-// Backward a block takes many items, and they are kept to four fillings, so
-// that the blocks' shares come out even.
-void plan_side(Side* s, int tokens, int rows_in_flight, int num_sms, bool back) {
-  if (s->H == 0) {
-    s->tile = 1;
-    s->hc = 1;
-    s->hsplit = 1;
-    s->items = 0;
-    return;
-  }
-  s->tile = s->H >= rows_in_flight ? 1 : (rows_in_flight + s->H - 1) / s->H;
-  if (s->tile > kTileTokens) s->tile = kTileTokens;
-  const int tiles = (tokens + s->tile - 1) / s->tile;
-  s->hc = tiles >= 4 * num_sms || s->H < rows_in_flight ? s->H : rows_in_flight;
-  if (back && s->hc > 4 * rows_in_flight) s->hc = 4 * rows_in_flight;
-  s->hsplit = (s->H + s->hc - 1) / s->hc;
-  s->items = tiles * s->hsplit;
-}
-
-// blocks of each side in the backward pass: the resident ones shared by rows,
-// each side that has rows with at least one
-void plan_blocks(NrParams* p, int resident) {
-  const long long q = p->side[0].H, k = p->side[1].H;
-  for (Side& s : p->side) {
-    long long n = s.H == 0 ? 0 : resident * (long long)s.H / (q + k);
-    if (s.H > 0 && n < 1) n = 1;
-    if (n > s.items) n = s.items;
-    s.blocks = (int)n;
-  }
-}
 int lanes_of(int D) { return D <= 64 ? 8 : D <= 640 ? 16 : 32; }
-int resident_blocks(int D, int num_sms) {
-  return num_sms * (D <= 256 ? bwd_blocks_per_sm<1>() : bwd_blocks_per_sm<4>());
+
+int rows_at_once(int D, bool back) {   // GP * U of the kernel
+  const int gp = 32 / lanes_of(D);
+  return gp * (D <= 128 ? (back ? 2 : 4) : D <= 256 ? 2 : 1);
 }
 
-template <int G, int V, int MODE>
-cudaError_t launch_mode(const LaunchCtx& c, const NrParams& p, bool back) {
-  size_t smem = (size_t)kTileTokens * (p.rope / 2) * sizeof(float2);
-  if (!back) {
-    norm_rope_kernel<G, V, MODE><<<p.side[0].items + p.side[1].items, kThreads, smem, c.stream>>>(p);
-  } else {
-    const size_t red = (size_t)(kThreads / 32) * G * V * 8 * sizeof(float);
-    if (red > smem) smem = red;
-    norm_rope_bwd_kernel<G, V, MODE><<<p.side[0].blocks + p.side[1].blocks, kThreads, smem, c.stream>>>(p);
+// Rows of a tile: kTileBytes of them, in full steps of a warp.
+int tile_rows(int D, bool back) {
+  const int g = rows_at_once(D, back);
+  int rt = kTileBytes / (D * (back ? 4 : 2)) / g * g;
+  if (rt > kMaxTileRows) rt = kMaxTileRows;
+  return rt < g ? g : rt;
+}
+
+// Tokens that a tile of a side with H heads touches, at most.
+int tile_tokens(int rt, int H) { return H == 0 ? 0 : H == 1 ? rt : (rt - 2) / H + 2; }
+
+int tensor_bytes_of(int D, bool back) { return (tile_rows(D, back) * D * 2 + 127) / 128 * 128; }
+
+int warp_bytes_of(const dsa_norm_rope_desc* d, bool back) {
+  const int rt = tile_rows(d->D, back);
+  const int tq = tile_tokens(rt, d->Hq), tk = tile_tokens(rt, d->Hk);
+  const int angles = (tq > tk ? tq : tk) * (d->rope_cols / 2) * (int)sizeof(float2);
+  return kStages * (back ? 2 : 1) * tensor_bytes_of(d->D, back) + (angles + 127) / 128 * 128;
+}
+
+size_t smem_of(const dsa_norm_rope_desc* d, bool back) {
+  const size_t n = (size_t)kWarps * warp_bytes_of(d, back);
+  const size_t red = back ? (size_t)kWarps * 1024 * sizeof(float) : 0;   // at most: G V 8 <= 1024
+  return n > red ? n : red;
+}
+
+// Blocks resident at once: what shared memory and registers allow.
+int resident_blocks(const dsa_norm_rope_desc* d, bool back, int num_sms) {
+  int n = (int)(227 * 1024 / (smem_of(d, back) + 1280));
+  const int regs = blocks_per_sm(d->D > 256 ? 4 : 1, back);
+  if (n > regs) n = regs;
+  return (n < 1 ? 1 : n) * num_sms;
+}
+
+// The resident blocks shared between the sides by rows (a token's angles count
+// as one more), each side that has rows with at least one and no more than
+// one tile a warp makes use of.
+void plan(NrParams* p, int tokens, int resident) {
+  const long long all = p->side[0].H + p->side[1].H + 2;
+  for (Side& s : p->side) {
+    s.rows = tokens * s.H;
+    s.tiles = (s.rows + p->rt - 1) / p->rt;
+    s.inv_H = s.H > 0 ? 1.f / (float)s.H : 0.f;
+    long long n = s.H == 0 ? 0 : (long long)resident * (s.H + 1) / all;
+    if (s.H > 0 && n < 1) n = 1;
+    const int most = (s.tiles + kWarps - 1) / kWarps;
+    s.blocks = (int)(n < most ? n : most);
   }
+}
+
+template <int G, int V, int MODE, bool BACK>
+cudaError_t launch_mode(const LaunchCtx& c, const NrParams& p, size_t smem) {
+  auto kern = norm_rope_kernel<G, V, MODE, BACK>;
+  if (smem > 40 * 1024) {   // with the static barriers, past 48 KB only on request
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<p.side[0].blocks + p.side[1].blocks, kThreads, smem, c.stream>>>(p);
   note_launches(1);
   return cudaGetLastError();
 }
-// Half-split pairs lie r/2 columns apart: r/16 lanes when that is a power of
-// two below G and the rotated range starts on a multiple of r columns.
 template <int G, int V>
-cudaError_t launch_gv(const LaunchCtx& c, const NrParams& p, bool inter, bool back) {
-  if (p.rope == 0) return launch_mode<G, V, kNone>(c, p, back);
-  if (inter) return launch_mode<G, V, kInter>(c, p, back);
-  const int lanes = p.rope / 16;
-  const bool shfl = (lanes & (lanes - 1)) == 0 && lanes < G && (p.D - p.rope) % p.rope == 0;
-  return shfl ? launch_mode<G, V, kShfl>(c, p, back) : launch_mode<G, V, kHalf>(c, p, back);
+cudaError_t launch_gv(const LaunchCtx& c, const NrParams& p, bool inter, bool back, size_t sm) {
+  if (p.rope == 0) return back ? launch_mode<G, V, kNone, true>(c, p, sm) : launch_mode<G, V, kNone, false>(c, p, sm);
+  if (inter) return back ? launch_mode<G, V, kInter, true>(c, p, sm) : launch_mode<G, V, kInter, false>(c, p, sm);
+  return back ? launch_mode<G, V, kHalf, true>(c, p, sm) : launch_mode<G, V, kHalf, false>(c, p, sm);
 }
-cudaError_t launch_nr(const LaunchCtx& c, const NrParams& p, bool inter, bool back) {
-  if (p.D <= 64) return launch_gv<8, 1>(c, p, inter, back);
-  if (p.D <= 128) return launch_gv<16, 1>(c, p, inter, back);
-  if (p.D <= 256) return launch_gv<16, 2>(c, p, inter, back);
-  if (p.D <= 640) return launch_gv<16, 5>(c, p, inter, back);
-  return launch_gv<32, 4>(c, p, inter, back);
+cudaError_t launch_nr(const LaunchCtx& c, const NrParams& p, const dsa_norm_rope_desc* d, bool back) {
+  const bool inter = d->interleaved != 0;
+  const size_t sm = smem_of(d, back);
+  if (p.D <= 64) return launch_gv<8, 1>(c, p, inter, back, sm);
+  if (p.D <= 128) return launch_gv<16, 1>(c, p, inter, back, sm);
+  if (p.D <= 256) return launch_gv<16, 2>(c, p, inter, back, sm);
+  if (p.D <= 640) return launch_gv<16, 5>(c, p, inter, back, sm);
+  return launch_gv<32, 4>(c, p, inter, back, sm);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -473,7 +539,7 @@ dsa_status check_desc(const dsa_shape* s, const dsa_norm_rope_desc* d) {
       d->rope_cols > 2 * kMaxHalf || d->Hq > 1024 || d->Hk > 1024)
     return DSA_ERR_UNSUPPORTED;
   // rows of a launch count as an int
-  if ((long long)s->B * s->T * (d->Hq + d->Hk) >= (1LL << 31)) return DSA_ERR_UNSUPPORTED;
+  if ((long long)s->B * s->T * (d->Hq + d->Hk) >= (1LL << 31) - kMaxTileRows) return DSA_ERR_UNSUPPORTED;
   return DSA_OK;
 }
 
@@ -481,19 +547,22 @@ NrParams make_params(const LaunchCtx& c, const dsa_shape* s, const dsa_norm_rope
   NrParams p = {};
   p.map = api_kv_map(s);
   p.inv_freq = d->inv_freq;
-  p.tokens = s->B * s->T;
   p.T = s->T;
   p.D = d->D;
   p.norm = d->norm_cols;
   p.rope = d->rope_cols;
+  p.rt = tile_rows(d->D, back);
+  p.tensor_bytes = tensor_bytes_of(d->D, back);
+  p.warp_bytes = warp_bytes_of(d, back);
   p.inv_norm = d->norm_cols > 0 ? 1.f / (float)d->norm_cols : 0.f;
   p.eps = d->eps;
+  p.wait_ns = c.wait_ns;
   p.err = c.err;
   p.side[0].H = d->Hq;
   p.side[1].H = d->Hk;
   p.side[0].w = d->q_weight;
   p.side[1].w = d->k_weight;
-  for (Side& sd : p.side) plan_side(&sd, p.tokens, kThreads / lanes_of(d->D), c.num_sms, back);
+  plan(&p, s->B * s->T, resident_blocks(d, back, c.num_sms));
   return p;
 }
 
@@ -510,7 +579,7 @@ extern "C" size_t dsa_norm_rope_workspace_size(const dsa_shape* s, const dsa_nor
   if (check_desc(s, d) != DSA_OK) return 0;
   // a row of partial sums for each resident block, one more for a side that
   // would have had none; sized for 256 SMs, so that it depends on no device
-  return ((size_t)resident_blocks(d->D, 256) + 2) * (d->norm_cols > 0 ? d->norm_cols : 1) * sizeof(float);
+  return ((size_t)resident_blocks(d, true, 256) + 2) * (d->norm_cols > 0 ? d->norm_cols : 1) * sizeof(float);
 }
 
 extern "C" dsa_status dsa_norm_rope(const dsa_shape* s, const dsa_norm_rope_desc* d, const uint16_t* q,
@@ -525,7 +594,7 @@ extern "C" dsa_status dsa_norm_rope(const dsa_shape* s, const dsa_norm_rope_desc
   p.side[0].y = q_out;
   p.side[1].x = k;
   p.side[1].y = k_out;
-  return launch_nr(c, p, d->interleaved != 0, false) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  return launch_nr(c, p, d, false) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
 extern "C" dsa_status dsa_norm_rope_backward(const dsa_shape* s, const dsa_norm_rope_desc* d, const uint16_t* q,
@@ -540,7 +609,6 @@ extern "C" dsa_status dsa_norm_rope_backward(const dsa_shape* s, const dsa_norm_
   if ((st = api_make_ctx(stream, &c)) != DSA_OK) return st;
   if (c.num_sms > 256) return DSA_ERR_UNSUPPORTED;
   NrParams p = make_params(c, s, d, true);
-  plan_blocks(&p, resident_blocks(d->D, c.num_sms));
   p.side[0].x = q;
   p.side[0].dy = dq_out;
   p.side[0].dx = dq;
@@ -563,7 +631,7 @@ extern "C" dsa_status dsa_norm_rope_backward(const dsa_shape* s, const dsa_norm_
       part += (size_t)p.side[i].blocks * p.norm;
     }
   }
-  if (launch_nr(c, p, d->interleaved != 0, true) != cudaSuccess) return DSA_ERR_CUDA;
+  if (launch_nr(c, p, d, true) != cudaSuccess) return DSA_ERR_CUDA;
   if (w.dw[0] != nullptr || w.dw[1] != nullptr) {
     norm_rope_dw_kernel<<<dim3((p.norm + 7) / 8, 2), 256, 0, c.stream>>>(w);
     note_launches(1);
