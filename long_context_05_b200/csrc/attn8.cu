@@ -833,7 +833,8 @@ __global__ void __launch_bounds__(kCombineThreads, 6) attn8_combine_kernel(const
 template <int DK, int DV, bool PAGED>
 cudaError_t launch_t(const LaunchCtx& c, const Params& p) {
   using C = Cfg<DK, DV>;
-  cudaError_t e = cudaFuncSetAttribute(attn8_kernel<DK, DV, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
+  static std::atomic<int> granted[kMaxDevices];
+  cudaError_t e = grant_smem(attn8_kernel<DK, DV, PAGED>, C::BYTES, c.device, granted);
   if (e != cudaSuccess) return e;
   attn8_kernel<DK, DV, PAGED><<<(unsigned)((long long)p.rows * p.nsplit * p.hsplit), kThreads, C::BYTES, c.stream>>>(p);
   note_launches(1);

@@ -30,6 +30,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kLanes = 8;                          // lanes per row
 constexpr int kRows = kThreads / kLanes;           // rows per block and step
+constexpr int kQRows = 4;                          // index query rows of a group in flight (short rows, many of them)
 constexpr int kMinExp = -48;
 
 __device__ __forceinline__ float max_abs8(const uint4& v) {
@@ -60,41 +61,56 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
-// One row of D columns by eight lanes: V vectors of eight columns each.
-template <int V>
-__device__ __forceinline__ void quantise_row(const uint16_t* src, int D, uint8_t* dst, float* scale, int gl, bool on) {
-  uint4 v[V];
-  float amax = 0.f;
+// R rows of D columns by eight lanes, V vectors of eight columns each; row i
+// lies at src[i] (null: none).  Every load is issued before the first is used.
+template <int V, int R>
+__device__ __forceinline__ void quantise_rows(const uint16_t* const (&src)[R], int D, uint8_t* const (&dst)[R],
+                                              float* const (&scale)[R], int gl) {
+  uint4 v[R][V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int col = (j * kLanes + gl) * 8;
-    v[j] = make_uint4(0u, 0u, 0u, 0u);
-    if (on && col < D) v[j] = *reinterpret_cast<const uint4*>(src + col);
-    amax = fmaxf(amax, max_abs8(v[j]));
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int col = (j * kLanes + gl) * 8;
+      v[i][j] = make_uint4(0u, 0u, 0u, 0u);
+      if (src[i] != nullptr && col < D) v[i][j] = *reinterpret_cast<const uint4*>(src[i] + col);
+    }
+  float amax[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    amax[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) amax[i] = fmaxf(amax[i], max_abs8(v[i][j]));
   }
 #pragma unroll
-  for (int d = 1; d < kLanes; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-  if (!on) return;
-  const int e = min(row_exponent(amax), 120);
-  if (e == 120) {
-    // 2^120 times a byte past 240 is 2^128, not an FP32 number: such values
-    // (1.875 * 2^127 and up) are stored as 240, so that the row stays finite
+  for (int d = 1; d < kLanes; d <<= 1)
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[j] = make_uint4(clamp2(v[j].x), clamp2(v[j].y), clamp2(v[j].z), clamp2(v[j].w));
+    for (int i = 0; i < R; ++i) amax[i] = fmaxf(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], d));
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (src[i] == nullptr) continue;
+    const int e = min(row_exponent(amax[i]), 120);
+    if (e == 120) {
+      // 2^120 times a byte past 240 is 2^128, not an FP32 number: such values
+      // (1.875 * 2^127 and up) are stored as 240, so that the row stays finite
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        v[i][j] = make_uint4(clamp2(v[i][j].x), clamp2(v[i][j].y), clamp2(v[i][j].z), clamp2(v[i][j].w));
+    }
+    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int col = (j * kLanes + gl) * 8;
+      if (col >= D) continue;
+      const uint32_t u[4] = {v[i][j].x, v[i][j].y, v[i][j].z, v[i][j].w};
+      uint32_t q[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        q[x] = e4m3x2(__uint_as_float(u[x] << 16) * inv, __uint_as_float(u[x] & 0xffff0000u) * inv);
+      *reinterpret_cast<uint2*>(dst[i] + col) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+    }
+    if (gl == 0) *scale[i] = __uint_as_float((uint32_t)(127 + e) << 23);
   }
-  const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int col = (j * kLanes + gl) * 8;
-    if (col >= D) continue;
-    const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-    uint32_t q[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      q[i] = e4m3x2(__uint_as_float(u[i] << 16) * inv, __uint_as_float(u[i] & 0xffff0000u) * inv);
-    *reinterpret_cast<uint2*>(dst + col) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-  }
-  if (gl == 0) *scale = __uint_as_float((uint32_t)(127 + e) << 23);
 }
 
 struct WriteParams {
@@ -125,18 +141,27 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(WriteParams p) {
     const bool keys = blk >= p.kv_blocks;
     if (keys) blk -= p.kv_blocks;
     const int n = blk * kRows + grp;
-    bool on = n < p.tokens;
-    const long long r = on ? new_row<PAGED>(p.map, n, p.T, p.err, gl == 0) : -1;
-    on = r >= 0;
-    if (!keys)
-      quantise_row<VK>(p.kv + (size_t)n * p.d_k, p.d_k, p.kv8 + r * p.d_k, p.kv_scale + r, gl, on);
-    else
-      quantise_row<VI>(p.kI + (size_t)n * p.D_I, p.D_I, p.kI8 + r * p.D_I, p.kI_scale + r, gl, on);
+    const long long r = n < p.tokens ? new_row<PAGED>(p.map, n, p.T, p.err, gl == 0) : -1;
+    const int D = keys ? p.D_I : p.d_k;
+    const uint16_t* const src[1] = {r >= 0 ? (keys ? p.kI : p.kv) + (size_t)n * D : nullptr};
+    uint8_t* const dst[1] = {(keys ? p.kI8 : p.kv8) + r * D};
+    float* const sc[1] = {(keys ? p.kI_scale : p.kv_scale) + r};
+    if (!keys) quantise_rows<VK, 1>(src, D, dst, sc, gl);
+    else quantise_rows<VI, 1>(src, D, dst, sc, gl);
     return;
   }
   blk -= p.kv_blocks + p.kI_blocks;
-  const long long n = (long long)blk * kRows + grp;
-  quantise_row<VI>(p.qI + n * p.D_I, p.D_I, p.qI8 + n * p.D_I, p.qI_scale + n, gl, n < (long long)p.tokens * p.H_I);
+  const uint16_t* src[kQRows];
+  uint8_t* dst[kQRows];
+  float* sc[kQRows];
+#pragma unroll
+  for (int i = 0; i < kQRows; ++i) {
+    const long long n = ((long long)blk * kQRows + i) * kRows + grp;
+    src[i] = n < (long long)p.tokens * p.H_I ? p.qI + n * p.D_I : nullptr;
+    dst[i] = p.qI8 + n * p.D_I;
+    sc[i] = p.qI_scale + n;
+  }
+  quantise_rows<VI, kQRows>(src, p.D_I, dst, sc, gl);
 }
 
 struct ReadParams {
@@ -255,7 +280,7 @@ extern "C" dsa_status dsa_cache_write(const dsa_shape* s, const uint16_t* kv, ui
   p.err = c.err;
   p.kv_blocks = kv ? (int)blocks_for(tokens) : 0;
   p.kI_blocks = k_I ? (int)blocks_for(tokens) : 0;
-  const unsigned blocks = p.kv_blocks + p.kI_blocks + (q_I ? blocks_for(tokens * s->H_I) : 0);
+  const unsigned blocks = p.kv_blocks + p.kI_blocks + (q_I ? blocks_for((tokens * s->H_I + kQRows - 1) / kQRows) : 0);
   return DSA_CACHE8_DISPATCH(write_t, c, p, blocks) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 

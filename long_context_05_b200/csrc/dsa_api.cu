@@ -19,7 +19,6 @@ void note_launches(int n) { g_launches.fetch_add((unsigned long long)n, std::mem
 
 namespace {
 
-constexpr int kMaxDevices = 64;
 constexpr long long kDefaultWaitNs = 2000000000LL;  // 2 s per bounded wait
 long long g_wait_ns = kDefaultWaitNs;
 

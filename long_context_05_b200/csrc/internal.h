@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "dsa.h"
 
 namespace dsa {
@@ -164,6 +166,21 @@ struct Attn8Args {
 
 // counts every kernel launch (dsa_launch_count)
 void note_launches(int n);
+
+// Dynamic shared memory past what a kernel is allowed by itself: asked for
+// once per kernel and device (`granted`: the kernel's own array, bytes granted
+// so far), since asking costs a launch a fifth of its time.
+constexpr int kMaxDevices = 64;
+template <class Kernel>
+cudaError_t grant_smem(Kernel kernel, int bytes, int device, std::atomic<int>* granted) {
+  if (bytes <= granted[device].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  int seen = granted[device].load(std::memory_order_relaxed);
+  while (seen < bytes && !granted[device].compare_exchange_weak(seen, bytes, std::memory_order_release)) {
+  }
+  return cudaSuccess;
+}
 
 // Launch with programmatic stream serialization: the kernel may start while
 // the one before it on the stream finishes, and must call pdl_wait

@@ -15,9 +15,9 @@
 // of memory whatever its heads and tokens.  Every warp works by itself: it
 // takes a run of tiles of about 4.5 KB and keeps kStages of them on their way
 // into shared memory of its own by bulk copies, so no registers hold loads in
-// flight and no warp waits for another.  A row is worked on by G lanes (16 up
-// to 640 columns; U rows of each group at a time where rows are short, for
-// independent work), reduced by shuffles and written once by 16-byte stores.
+// flight and no warp waits for another.  A row is worked on by G lanes (16 at
+// 576 columns, 8 at 128; U rows of each group at a time where rows are short,
+// for independent work), reduced by shuffles and written once by 16-byte stores.
 // The r/2 sines and cosines of a token are formed once per warp and token.
 // The angle is reduced in FP64 (pos times f is exact to 2^-53 there; FP32
 // would be off by 2^-24 of the whole angle, half a degree at position 128K),
@@ -114,15 +114,12 @@ __device__ __forceinline__ uint4 pack8(const F8& f) {
   }
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
-__device__ __forceinline__ F8 load_w(const float* w, int col) {
+// Weights of the columns 8 i .. 8 i + 7 from their copy in shared memory: the
+// first four of every eight, then the second four, so that neighbouring lanes
+// read neighbouring 16 bytes.
+__device__ __forceinline__ F8 load_w(const ulonglong2* sW, int nvec, int i) {
+  const ulonglong2 a = sW[i], b = sW[nvec + i];
   F8 f;
-  if (w == nullptr) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f.v[i] = pair(1.f, 1.f);
-    return f;
-  }
-  const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2*>(w + col));
-  const ulonglong2 b = __ldg(reinterpret_cast<const ulonglong2*>(w + col) + 1);
   f.v[0] = a.x; f.v[1] = a.y; f.v[2] = b.x; f.v[3] = b.y;
   return f;
 }
@@ -174,14 +171,14 @@ __device__ __forceinline__ void rotate8(F8& z, const F8& o, const float2* cs, in
 }
 
 // Blocks of an SM that the registers leave room for.
-constexpr int blocks_per_sm(int V, bool back) { return V >= 4 ? (back ? 3 : 5) : (back ? 5 : 6); }
+constexpr int blocks_per_sm(int V, bool back) { return V >= 4 ? (back ? 3 : 5) : (back ? 4 : 5); }
 
 template <int G, int V, int MODE, bool BACK>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(V, BACK)) norm_rope_kernel(NrParams p) {
   extern __shared__ uint4 smem4[];
   __shared__ uint64_t full_bar[kWarps][kStages];
   constexpr int GP = 32 / G;                      // groups of a warp
-  constexpr int U = V == 1 ? (BACK ? 2 : 4) : V == 2 ? 2 : 1;
+  constexpr int U = V <= 2 ? 2 : 1;
   constexpr bool HOIST = V <= 2;                  // weights stay in registers
   constexpr int kTensors = BACK ? 2 : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -212,16 +209,27 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(V, BACK)) norm_rope_ke
     for (int i = tile0; i < tile1 && i < tile0 + kStages; ++i) load_tile(i);
   }
   __syncwarp();
+  // the weights' copy, behind the warps' rings (ones where there are none)
+  const int nvec = p.norm >> 3;
+  ulonglong2* sW = reinterpret_cast<ulonglong2*>(reinterpret_cast<uint8_t*>(smem4) + kWarps * p.warp_bytes);
+  for (int i = threadIdx.x; i < 2 * nvec; i += kThreads) {
+    const float4 w4 = s.w != nullptr ? __ldg(reinterpret_cast<const float4*>(s.w) + i) : make_float4(1.f, 1.f, 1.f, 1.f);
+    *reinterpret_cast<float4*>(sW + (i & 1) * nvec + (i >> 1)) = w4;
+  }
+  __syncthreads();
   F8 wr[HOIST ? V : 1];
   if constexpr (HOIST) {
 #pragma unroll
     for (int j = 0; j < V; ++j)
-      if ((j * G + gl) * 8 < p.norm) wr[j] = load_w(s.w, (j * G + gl) * 8);
+      if ((j * G + gl) * 8 < p.norm) wr[j] = load_w(sW, nvec, j * G + gl);
   }
-  auto weights = [&](int j, int col) -> F8 {
+  auto weights = [&](int j) -> F8 {
     if constexpr (HOIST) return wr[j];
-    else return load_w(s.w, col);
+    else return load_w(sW, nvec, j * G + gl);
   };
+  // steps of G * 8 columns that lie wholly in the normalised columns, and of
+  // those the ones with no rotated column: there no lane decides for itself
+  const int jn = p.norm / (G * 8), jf = min(p.norm, MODE == kNone ? p.D : r0) / (G * 8);
   F8 acc[BACK ? V : 1];
   if constexpr (BACK) {
 #pragma unroll
@@ -252,32 +260,27 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(V, BACK)) norm_rope_ke
     const uint8_t* sA = ring + st * kTensors * p.tensor_bytes;     // x forward, dy backward
     for (int rr = 0; rr < nr; rr += GP * U) {
       int r[U];
-      uint4 v[U][V];
+      const uint4* ra[U];                          // this lane's first columns of the row
       uint64_t ss2[U], dot2[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         r[u] = min(rr + u * GP + grp, nr - 1);    // groups past the tile follow its last row and write nothing
+        ra[u] = reinterpret_cast<const uint4*>(sA + r[u] * p.D * 2) + gl;
         ss2[u] = dot2[u] = 0ull;
-        const uint4* ra = reinterpret_cast<const uint4*>(sA + r[u] * p.D * 2);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const int col = (j * G + gl) * 8;
-          v[u][j] = make_uint4(0u, 0u, 0u, 0u);
-          if (col < p.D) v[u][j] = ra[col >> 3];
-        }
       }
       // the angles of row r: its token within those of cs ((off + r) / H by
       // the reciprocal: both below 2^11, exact with the half)
       auto angles = [&](int r_) -> const float2* {
         return cs + (n0 - n_lo + (int)(((float)(off + r_) + 0.5f) * s.inv_H)) * half;
       };
+      // columns `col` of the partner range (col rotated)
       auto partner = [&](int u, int col) -> F8 {
         const int pc = col - r0 < half ? col + half : col - half;
-        return unpack8(*reinterpret_cast<const uint4*>(sA + r[u] * p.D * 2 + pc * 2));
+        return unpack8(ra[u][(pc >> 3) - gl]);
       };
       // backward: g = R^T dy at this lane's columns of step j
       auto rotated = [&](int u, int j, int col) -> F8 {
-        F8 f = unpack8(v[u][j]);
+        F8 f = unpack8(ra[u][j * G]);
         if (MODE != kNone && col >= r0) {
           F8 q = f;
           if constexpr (MODE == kHalf) q = partner(u, col);
@@ -285,30 +288,34 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(V, BACK)) norm_rope_ke
         }
         return f;
       };
-      auto x_of = [&](int u, int col) -> F8 {
-        return unpack8(*reinterpret_cast<const uint4*>(sA + p.tensor_bytes + r[u] * p.D * 2 + col * 2));
+      auto x_of = [&](int u, int j) -> F8 {
+        return unpack8(*reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(ra[u] + j * G) + p.tensor_bytes));
       };
+      // 1. the sums of squares, backward also of w g x
+      F8 x[BACK ? 1 : U][BACK ? 1 : V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int col = (j * G + gl) * 8;
-        if (col < p.norm) {
-          if constexpr (!BACK) {
+        if constexpr (!BACK) {
+          if (j < jn || col < p.D) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-              const F8 f = unpack8(v[u][j]);
+            for (int u = 0; u < U; ++u) x[u][j] = unpack8(ra[u][j * G]);
+          }
+          if (j < jn || col < p.norm) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) ss2[u] = fma2(f.v[i], f.v[i], ss2[u]);
-            }
-          } else {
-            const F8 w = weights(j, col);
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-              const F8 f = rotated(u, j, col), x = x_of(u, col);
+              for (int i = 0; i < 4; ++i) ss2[u] = fma2(x[u][j].v[i], x[u][j].v[i], ss2[u]);
+          }
+        } else if (j < jn || col < p.norm) {
+          const F8 w = weights(j);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                ss2[u] = fma2(x.v[i], x.v[i], ss2[u]);
-                dot2[u] = fma2(mul2(f.v[i], x.v[i]), w.v[i], dot2[u]);
-              }
+          for (int u = 0; u < U; ++u) {
+            const F8 f = j < jf ? unpack8(ra[u][j * G]) : rotated(u, j, col), xr = x_of(u, j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              ss2[u] = fma2(xr.v[i], xr.v[i], ss2[u]);
+              dot2[u] = fma2(mul2(f.v[i], xr.v[i]), w.v[i], dot2[u]);
             }
           }
         }
@@ -328,61 +335,79 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(V, BACK)) norm_rope_ke
           if (BACK) dot[u] += __shfl_xor_sync(lane_grp, dot[u], d);
         }
       uint64_t rho[U], c1[U];
+      uint4* dst[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const float h = rsqrtf(fmaf(ss[u], p.inv_norm, p.eps));
         const float c = -(h * h * h * dot[u] * p.inv_norm);
         rho[u] = pair(h, h);
         c1[u] = pair(c, c);
+        dst[u] = reinterpret_cast<uint4*>((BACK ? s.dx : s.y) + (size_t)(row0 + r[u]) * p.D) + gl;
       }
+      // dx at normalised columns, from g and x; the weight sums
+      auto grad = [&](int u, int j, const F8& f, const F8& w) -> F8 {
+        const F8 xr = x_of(u, j);
+        F8 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t gr = mul2(f.v[i], rho[u]);
+          acc[BACK ? j : 0].v[i] = fma2(gr, xr.v[i], acc[BACK ? j : 0].v[i]);
+          o.v[i] = fma2(gr, w.v[i], mul2(c1[u], xr.v[i]));
+        }
+        return o;
+      };
+      auto live = [&](int u) { return ok && rr + u * GP + grp < nr; };
+      // 2. the rows out
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int col = (j * G + gl) * 8;
-        if (col >= p.D) continue;
-        const bool rot = MODE != kNone && col >= r0, nrm = col < p.norm;
-        F8 w = {};
-        if (nrm) w = weights(j, col);
+        if (j < jf) {
+          const F8 w = weights(j);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (!ok || rr + u * GP + grp >= nr) continue;
-          uint4* dst = reinterpret_cast<uint4*>((BACK ? s.dx : s.y) + (size_t)(row0 + r[u]) * p.D + col);
-          if (!nrm && !rot) {
-            *dst = v[u][j];
-            continue;
-          }
-          F8 f;
-          if constexpr (!BACK) {
-            f = unpack8(v[u][j]);
-            if (nrm) {
+          for (int u = 0; u < U; ++u) {
+            if (!live(u)) continue;
+            F8 o;
+            if constexpr (BACK) {
+              o = grad(u, j, unpack8(ra[u][j * G]), w);
+            } else {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) f.v[i] = mul2(mul2(f.v[i], rho[u]), w.v[i]);
+              for (int i = 0; i < 4; ++i) o.v[i] = mul2(mul2(x[u][j].v[i], rho[u]), w.v[i]);
             }
-            if (rot) {
-              F8 g = f;
-              if constexpr (MODE == kHalf) {
-                const int pc = col - r0 < half ? col + half : col - half;
-                g = partner(u, col);
-                if (pc < p.norm) {
-                  const F8 wp = load_w(s.w, pc);
+            dst[u][j * G] = pack8(o);
+          }
+        } else if (col < p.D) {
+          const bool rot = MODE != kNone && col >= r0, nrm = col < p.norm;
+          F8 w = {};
+          if (nrm) w = weights(j);
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) g.v[i] = mul2(mul2(g.v[i], rho[u]), wp.v[i]);
+          for (int u = 0; u < U; ++u) {
+            if (!live(u)) continue;
+            F8 f;
+            if constexpr (BACK) {
+              f = rotated(u, j, col);
+              if (nrm) f = grad(u, j, f, w);
+            } else {
+              f = x[u][j];
+              if (nrm) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f.v[i] = mul2(mul2(f.v[i], rho[u]), w.v[i]);
+              }
+              if (rot) {
+                F8 g = f;
+                if constexpr (MODE == kHalf) {
+                  const int pc = col - r0 < half ? col + half : col - half;
+                  g = partner(u, col);
+                  if (pc < p.norm) {
+                    const F8 wp = load_w(sW, nvec, pc >> 3);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) g.v[i] = mul2(mul2(g.v[i], rho[u]), wp.v[i]);
+                  }
                 }
-              }
-              rotate8<MODE>(f, g, angles(r[u]), col - r0, half, false);
-            }
-          } else {
-            f = rotated(u, j, col);
-            if (nrm) {
-              const F8 x = x_of(u, col);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint64_t gr = mul2(f.v[i], rho[u]);
-                acc[j].v[i] = fma2(gr, x.v[i], acc[j].v[i]);
-                f.v[i] = fma2(gr, w.v[i], mul2(c1[u], x.v[i]));
+                rotate8<MODE>(f, g, angles(r[u]), col - r0, half, false);
               }
             }
+            dst[u][j * G] = pack8(f);
           }
-          *dst = pack8(f);
         }
       }
     }
@@ -440,17 +465,18 @@ __global__ void __launch_bounds__(256) norm_rope_dw_kernel(DwParams p) {
   }
 }
 
-int lanes_of(int D) { return D <= 64 ? 8 : D <= 640 ? 16 : 32; }
+// Lanes of a row: few, so that a warp's shuffles, square roots and addresses
+// serve many rows, with at most five steps of registers each.
+int lanes_of(int D) { return D <= 64 ? 4 : D <= 128 ? 8 : D <= 640 ? 16 : 32; }
 
-int rows_at_once(int D, bool back) {   // GP * U of the kernel
-  const int gp = 32 / lanes_of(D);
-  return gp * (D <= 128 ? (back ? 2 : 4) : D <= 256 ? 2 : 1);
-}
+int rows_at_once(int D) { return 32 / lanes_of(D) * (D <= 256 ? 2 : 1); }   // GP * U of the kernel
 
-// Rows of a tile: kTileBytes of them, in full steps of a warp.
+// Rows of a tile: kTileBytes of them (half that for short rows, which need
+// more warps and less each: 99 -> 94 us on 4096 tokens of 65 heads of 128),
+// in full steps of a warp.
 int tile_rows(int D, bool back) {
-  const int g = rows_at_once(D, back);
-  int rt = kTileBytes / (D * (back ? 4 : 2)) / g * g;
+  const int g = rows_at_once(D);
+  int rt = (D <= 256 ? kTileBytes / 2 : kTileBytes) / (D * (back ? 4 : 2)) / g * g;
   if (rt > kMaxTileRows) rt = kMaxTileRows;
   return rt < g ? g : rt;
 }
@@ -468,7 +494,7 @@ int warp_bytes_of(const dsa_norm_rope_desc* d, bool back) {
 }
 
 size_t smem_of(const dsa_norm_rope_desc* d, bool back) {
-  const size_t n = (size_t)kWarps * warp_bytes_of(d, back);
+  const size_t n = (size_t)kWarps * warp_bytes_of(d, back) + (size_t)d->norm_cols * sizeof(float);
   const size_t red = back ? (size_t)kWarps * 1024 * sizeof(float) : 0;   // at most: G V 8 <= 1024
   return n > red ? n : red;
 }
@@ -500,10 +526,9 @@ void plan(NrParams* p, int tokens, int resident) {
 template <int G, int V, int MODE, bool BACK>
 cudaError_t launch_mode(const LaunchCtx& c, const NrParams& p, size_t smem) {
   auto kern = norm_rope_kernel<G, V, MODE, BACK>;
-  if (smem > 40 * 1024) {   // with the static barriers, past 48 KB only on request
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  static std::atomic<int> granted[kMaxDevices];
+  const cudaError_t e = grant_smem(kern, (int)smem, c.device, granted);
+  if (e != cudaSuccess) return e;
   kern<<<p.side[0].blocks + p.side[1].blocks, kThreads, smem, c.stream>>>(p);
   note_launches(1);
   return cudaGetLastError();
@@ -517,8 +542,8 @@ cudaError_t launch_gv(const LaunchCtx& c, const NrParams& p, bool inter, bool ba
 cudaError_t launch_nr(const LaunchCtx& c, const NrParams& p, const dsa_norm_rope_desc* d, bool back) {
   const bool inter = d->interleaved != 0;
   const size_t sm = smem_of(d, back);
-  if (p.D <= 64) return launch_gv<8, 1>(c, p, inter, back, sm);
-  if (p.D <= 128) return launch_gv<16, 1>(c, p, inter, back, sm);
+  if (p.D <= 64) return launch_gv<4, 2>(c, p, inter, back, sm);
+  if (p.D <= 128) return launch_gv<8, 2>(c, p, inter, back, sm);
   if (p.D <= 256) return launch_gv<16, 2>(c, p, inter, back, sm);
   if (p.D <= 640) return launch_gv<16, 5>(c, p, inter, back, sm);
   return launch_gv<32, 4>(c, p, inter, back, sm);
