@@ -198,7 +198,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream():
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_get_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -209,7 +209,7 @@ def _need(t, dtype, name):
 
 
 def _check(fn, code):
-    if code != 0:
+    if code:
         raise DsaError(fn, code)
 
 
@@ -411,21 +411,31 @@ def forward(shape: Shape, inp: dict, out, lse, idx, ws, entry: str = "dsa_forwar
     return out, lse, idx
 
 
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _bad(t, dtype, numel, name):
+    raise ValueError(f"{name}: need a contiguous tensor of {numel} {dtype} on the current CUDA device, got "
+                     f"{tuple(t.shape)} {t.dtype} on {t.device} contiguous={t.is_contiguous()}")
+
+
 def _addresses(*specs):
     """Addresses of tensors, each checked: specs are (tensor or None, dtype,
     elements, name); contiguous, on the current device, of exactly that type
     and size.  None (left out) has no address."""
-    dev = -1
     out = []
+    dev = -2
     for t, dtype, numel, name in specs:
         if t is None:
             out.append(None)
             continue
-        if dev < 0:
-            dev = torch.cuda.current_device() if t.is_cuda else -2
-        if t.dtype is not dtype or t.numel() != numel or not t.is_contiguous() or t.get_device() != dev:
-            raise ValueError(f"{name}: need a contiguous tensor of {numel} {dtype} on the current CUDA device, got "
-                             f"{tuple(t.shape)} {t.dtype} on {t.device} contiguous={t.is_contiguous()}")
+        at = t.get_device()
+        if at != dev:                    # the first tensor, or one elsewhere
+            if dev >= 0 or at < 0 or at != _get_device():
+                _bad(t, dtype, numel, name)
+            dev = at
+        if t.dtype is not dtype or t.numel() != numel or not t.is_contiguous():
+            _bad(t, dtype, numel, name)
         out.append(t.data_ptr())
     return out
 
@@ -434,7 +444,7 @@ def _workspace(ws):
     """Address and bytes of a workspace tensor (or None)."""
     if ws is None:
         return None, 0
-    if not ws.is_contiguous() or not ws.is_cuda or ws.get_device() != torch.cuda.current_device():
+    if not ws.is_contiguous() or ws.get_device() < 0 or ws.get_device() != _get_device():
         raise ValueError(f"workspace: need a contiguous tensor on the current CUDA device, got {ws.device}")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
