@@ -210,38 +210,49 @@ __device__ __forceinline__ void tmem_scale(uint32_t addr, float alpha) {
   tmem_wait_st();
 }
 
-// Four head rows of q (rows 4 w .. 4 w + 3 of the CTA's 64) in two e4m3 terms:
-// the rows are contiguous, so a warp takes them in full steps of 32 vectors of
-// eight columns; a row's exponent comes from its maximum over the warp.
+// Four head rows of q (rows 4 w .. 4 w + 3 of the CTA's 64) in two e4m3 terms,
+// by one warp.  A step is 32 vectors of eight columns: the full steps of each
+// row, then what is left of the rows' columns, 32 / RV rows to a step, so that
+// a lane's place in shared memory is known once for all rows but for the
+// swizzle.  A row's exponent comes from its maximum over the warp.
 template <int DK>
 struct QRows {
-  static constexpr int VPR = DK / 8, NVEC = 4 * VPR, STEPS = (NVEC + 31) / 32;
+  static constexpr int FULL = DK / 256;                  // full steps of a row
+  static constexpr int RV = (DK - FULL * 256) / 8 <= 8 ? 8 : 16;   // lanes of a row in the last steps
+  static constexpr int TAILS = 4 * RV / 32;              // last steps
+  static constexpr int STEPS = 4 * FULL + TAILS;
   uint4 v[STEPS];
 };
 template <int DK>
 __device__ __forceinline__ void load_q_rows(QRows<DK>& q4, const uint16_t* q, int heads, int w, int lane) {
   using Q = QRows<DK>;
+  const uint16_t* q0 = q + (size_t)4 * w * DK;
 #pragma unroll
   for (int s = 0; s < Q::STEPS; ++s) {
-    const int i = s * 32 + lane;
+    const bool full = s < 4 * Q::FULL;
+    const int row = full ? s / (Q::FULL > 0 ? Q::FULL : 1) : (s - 4 * Q::FULL) * (32 / Q::RV) + lane / Q::RV;
+    const int col = full ? (s % (Q::FULL > 0 ? Q::FULL : 1)) * 256 + lane * 8 : Q::FULL * 256 + (lane % Q::RV) * 8;
     q4.v[s] = make_uint4(0u, 0u, 0u, 0u);
-    if (i < Q::NVEC && 4 * w + i / Q::VPR < heads)
-      q4.v[s] = __ldg(reinterpret_cast<const uint4*>(q + (size_t)4 * w * DK) + i);
+    if (4 * w + row < heads && col < DK) q4.v[s] = __ldg(reinterpret_cast<const uint4*>(q0 + row * DK + col));
   }
 }
 template <int DK, int DV>
 __device__ __forceinline__ void split_q_rows(const QRows<DK>& q4, int w, int lane, uint8_t* sQ, uint8_t* sP, float* sE) {
   using C = Cfg<DK, DV>;
-  constexpr int VPR = QRows<DK>::VPR, NVEC = QRows<DK>::NVEC, STEPS = QRows<DK>::STEPS;
-  const uint4* v = q4.v;
+  using Q = QRows<DK>;
   uint32_t m[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int s = 0; s < STEPS; ++s) {
-    const uint32_t x = max_abs8(v[s]);
-    const int row = (s * 32 + lane) / VPR;
+  for (int s = 0; s < Q::STEPS; ++s) {
+    const uint32_t x = max_abs8(q4.v[s]);
+    if (s < 4 * Q::FULL) {
+      m[s / (Q::FULL > 0 ? Q::FULL : 1)] = max(m[s / (Q::FULL > 0 ? Q::FULL : 1)], x);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i >= s * 32 / VPR && i <= (s * 32 + 31) / VPR) m[i] = max(m[i], row == i ? x : 0u);
+      for (int i = 0; i < 32 / Q::RV; ++i) {
+        const int row = (s - 4 * Q::FULL) * (32 / Q::RV) + i;
+        m[row] = max(m[row], lane / Q::RV == i ? x : 0u);
+      }
+    }
   }
   float inv[4];
 #pragma unroll
@@ -250,31 +261,32 @@ __device__ __forceinline__ void split_q_rows(const QRows<DK>& q4, int w, int lan
     inv[i] = __uint_as_float((uint32_t)(127 - e) << 23);
     if (lane == i) sE[4 * w + i] = __uint_as_float((uint32_t)(127 + e) << 23);
   }
-#pragma unroll
-  for (int s = 0; s < STEPS; ++s) {
-    const int i = s * 32 + lane, row = i / VPR, col = (i - row * VPR) * 8;
-    if (i >= NVEC) continue;
-    const float f = row == 0 ? inv[0] : row == 1 ? inv[1] : row == 2 ? inv[2] : inv[3];
-    const uint32_t x[4] = {v[s].x, v[s].y, v[s].z, v[s].w};
+  // both terms of eight columns: 8 bytes at d and at d + to_lo
+  auto put = [&](const uint4& v, float f, uint8_t* d, int to_lo) {
+    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int y = 0; y < 4; ++y) split2(__uint_as_float(x[y] << 16) * f, __uint_as_float(x[y] & 0xffff0000u) * f, hi[y], lo[y]);
-    const int rr = 4 * w + row, c16 = (col % 128) / 16, sub = col % 16;
-    uint8_t* d;
-    int to_lo;                                           // distance to the second term
-    if (col < C::QT) {
-      // staged in the P buffers: [term][atom][64 rows x 128 bytes]
-      d = sP + (col / 128) * (kM * 128) + rr * 128 + ((c16 ^ (rr & 7)) << 4) + sub;
-      to_lo = (C::QT / 128) * (kM * 128);
-    } else if (col < C::NF * 128) {
-      d = sQ + ((col - C::QT) / 128) * (kM * 128) + rr * 128 + ((c16 ^ (rr & 7)) << 4) + sub;
-      to_lo = C::QPIECE;
-    } else {
-      d = sQ + C::QSF * (kM * 128) + rr * 64 + ((((col - C::NF * 128) / 16) ^ ((rr >> 1) & 3)) << 4) + sub;
-      to_lo = C::QPIECE;
-    }
     *reinterpret_cast<uint2*>(d) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
     *reinterpret_cast<uint2*>(d + to_lo) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+  };
+#pragma unroll
+  for (int s = 0; s < Q::STEPS; ++s) {
+    if (s < 4 * Q::FULL) {
+      const int i = s / (Q::FULL > 0 ? Q::FULL : 1), u = s % (Q::FULL > 0 ? Q::FULL : 1), rr = 4 * w + i;
+      const int c16 = (lane & 15) >> 1, in_atom = (lane >> 4) * (kM * 128);
+      const int at = rr * 128 + ((c16 ^ (rr & 7)) << 4) + (lane & 1) * 8 + in_atom;
+      // q's TMEM columns are staged in the P buffers: [term][atom][64 rows x 128 bytes]
+      if (u * 256 < C::QT) put(q4.v[s], inv[i], sP + (u * 2) * (kM * 128) + at, (C::QT / 128) * (kM * 128));
+      else put(q4.v[s], inv[i], sQ + (u * 2 - C::QT / 128) * (kM * 128) + at, C::QPIECE);
+    } else {
+      const int i = (s - 4 * Q::FULL) * (32 / Q::RV) + lane / Q::RV, rr = 4 * w + i, l = lane % Q::RV;
+      if (Q::FULL * 256 + l * 8 >= DK) continue;
+      const float f = i == 0 ? inv[0] : i == 1 ? inv[1] : i == 2 ? inv[2] : inv[3];
+      uint8_t* d = C::TAIL != 0 ? sQ + C::QSF * (kM * 128) + rr * 64 + (((l >> 1) ^ ((rr >> 1) & 3)) << 4)
+                                : sQ + rr * 128 + (((l >> 1) ^ (rr & 7)) << 4);
+      put(q4.v[s], f, d + (l & 1) * 8, C::QPIECE);
+    }
   }
 }
 
@@ -321,12 +333,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
   const int slot0 = min(split * kc, nslots), slot1 = min(slot0 + kc, nslots);
   const int nchunks = (slot1 - slot0 + kN - 1) / kN;
 
-  // the softmax warps' rows of q (0..31) are on their way while the barriers
-  // and TMEM are set up; the gather warps take rows 32..63 behind their first
-  // chunk
+  const int32_t* irow = dense ? nullptr : p.idx + (size_t)row * p.k;
+  // index of slot s of this split; -1 past the end and for an empty slot
+  auto load_idx = [&](int s) -> int { return s < slot1 ? (dense ? s : irow[s]) : -1; };
+  // q's rows are on their way while the barriers and TMEM are set up: the
+  // softmax warps take rows 0..31, the gather warps 32..63, behind the indices
+  // of their first two chunks
+  const int kl = 16 * (warp - kFirstGather) + (lane & 15);
+  int i_cur = -1, i_next = -1;
+  if (warp >= kFirstGather) {
+    i_cur = load_idx(slot0 + kl);
+    i_next = load_idx(slot0 + kN + kl);
+  }
   QRows<DK> q4;
-  const uint16_t* q0 = p.q + ((size_t)row * p.H + hs * kM) * DK;
-  if (warp >= kFirstSoftmax && warp < kFirstGather) load_q_rows(q4, q0, p.H - hs * kM, warp - kFirstSoftmax, lane);
+  if (warp >= kFirstSoftmax)
+    load_q_rows(q4, p.q + ((size_t)row * p.H + hs * kM) * DK, p.H - hs * kM, warp - kFirstSoftmax, lane);
 
   if (threadIdx.x == 0) {
     mbar_init(q_ready, 8);
@@ -371,9 +392,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     const bool r = mbar_wait(bar, parity, p.wait_ns, ab);
     return __all_sync(0xffffffffu, r);
   };
-  const int32_t* irow = dense ? nullptr : p.idx + (size_t)row * p.k;
-  // index of slot s of this split; -1 past the end and for an empty slot
-  auto load_idx = [&](int s) -> int { return s < slot1 ? (dense ? s : irow[s]) : -1; };
   // cache row (relative to the sequence's first in a contiguous cache); -1
   // for no key and for an index outside [0, L_b)
   auto row_of = [&](int v) -> int {
@@ -387,12 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     // warp g copies keys [16 g, 16 g + 16) of every chunk
     const int g = warp - kFirstGather;
     const uint8_t* base = p.kv8 + base_row * DK;
-    const int kl = 16 * g + (lane & 15);
-    int r_cur = row_of(load_idx(slot0 + kl));
-    int i_next = load_idx(slot0 + kN + kl);
+    int r_cur = row_of(i_cur);
     // this warp's rows of q, behind the first chunk
     auto help_q = [&]() {
-      load_q_rows(q4, q0, p.H - hs * kM, warp - kFirstSoftmax, lane);
       split_q_rows<DK, DV>(q4, warp - kFirstSoftmax, lane, sQ, sP, sE);
       fence_proxy_async_smem();
       asm volatile("bar.arrive 1, 512;" ::: "memory");
@@ -445,21 +460,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
       if (PAGED && v >= 0 && r < 0 && hs == 0) report_error(p.err, DSA_ERR_DEVICE_BOUNDS, ERR_SITE_ATTN8 | (1u << 8));
       return r;
     };
-    int i_next[4];
+    int ip[4];
     float s_cur[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) i_next[u] = load_idx(slot0 + lane + 32 * u);
+    for (int u = 0; u < 4; ++u) ip[u] = load_idx(slot0 + lane + 32 * u);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      s_cur[u] = scale_of(checked_row(i_next[u]));
-      i_next[u] = load_idx(slot0 + kN + lane + 32 * u);
+      s_cur[u] = scale_of(checked_row(ip[u]));
+      ip[u] = load_idx(slot0 + kN + lane + 32 * u);
     }
     for (int j = 0; j < nchunks; ++j) {
       float s_next[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        s_next[u] = scale_of(checked_row(i_next[u]));
-        i_next[u] = load_idx(slot0 + (j + 2) * kN + lane + 32 * u);
+        s_next[u] = scale_of(checked_row(ip[u]));
+        ip[u] = load_idx(slot0 + (j + 2) * kN + lane + 32 * u);
       }
       const int pb = j & 1;
       if (j >= 2 && !wwait(&par_empty[pb], (uint32_t)(j / 2 - 1) & 1)) { fail(3); break; }
@@ -697,29 +712,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
       fail(12);
       ok = false;
     }
-    // The rows leave through the keys' regions (every MMA is done): a thread
-    // has 16-byte pieces of one row, which as stores of their own would touch
-    // 32 lines an instruction; a row goes out as one bulk copy.  The pitch
-    // keeps the pieces of eight rows on different banks.
-    constexpr int PITCH = DV * 2 + 16;
-    static_assert(kM * PITCH <= C::KV_BYTES, "output staging");
-    const bool write = ok && nchunks > 0;
+    // A thread has a quarter of one row in 16-byte pieces, which as stores of
+    // their own would touch 32 lines an instruction; it puts them side by side
+    // in the keys' regions (every MMA is done) and sends them out as bulk
+    // copies.  The pitch keeps the pieces of eight threads on different banks.
+    constexpr int TC = C::OCOLS / 2;                     // value columns of a thread
+    constexpr int PITCH = TC * 2 + 16;
+    static_assert(256 * PITCH <= C::KV_BYTES, "output staging");
     const size_t orow = p.nsplit == 1 ? (size_t)row : (size_t)row * p.nsplit + split;
-    if (write) {
+    if (ok && nchunks > 0) {
       tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      constexpr int W = C::OCOLS / 2 < 32 ? 16 : 32;
+      constexpr int W = TC < 32 ? 16 : 32;
       // TMEM column x of the accumulator: MMA x / (NV/2), its columns
-      // [kg NV/2, + NV/2) in this lane half
+      // [kg NV/2, + NV/2) in this lane half; a thread's columns are in one MMA
+      static_assert(TC <= C::NV / 2, "a thread's columns lie side by side");
+      const int v00 = c * TC / (C::NV / 2) * C::NV + kg * (C::NV / 2) + c * TC % (C::NV / 2);
+      uint8_t* mine = sKV + (sw * 32 + lane) * PITCH;
 #pragma unroll 1
-      for (int x0 = 0; x0 < C::OCOLS / 2; x0 += W) {
-        const int x = c * (C::OCOLS / 2) + x0;
-        const int v0 = x / (C::NV / 2) * C::NV + kg * (C::NV / 2) + x % (C::NV / 2);
+      for (int x0 = 0; x0 < TC; x0 += W) {
         uint32_t o[W];
-        if constexpr (W == 32) tmem_ld32(tmem + lane_addr + C::OCOL + x, o);
-        else tmem_ld16(tmem + lane_addr + C::OCOL + x, o);
+        if constexpr (W == 32) tmem_ld32(tmem + lane_addr + C::OCOL + c * TC + x0, o);
+        else tmem_ld16(tmem + lane_addr + C::OCOL + c * TC + x0, o);
         tmem_wait_ld_dep(o);
-        uint8_t* dst = sKV + r * PITCH + v0 * 2;
         float f = inv;
         if (p.nsplit > 1) {
           float mo = 0.f;
@@ -728,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
           // the power of two that brings the group's largest into [2^14, 2^15)
           const int e = min(max(127 + 14 - (int)(__float_as_uint(mo * inv) >> 23), -120), 126);
           f = inv * __uint_as_float((uint32_t)(127 + e) << 23);
-          if (head_ok) p.part_f[(orow * p.H + h) * (DV / W) + v0 / W] = __uint_as_float((uint32_t)(127 - e) << 23);
+          if (head_ok) p.part_f[(orow * p.H + h) * (DV / W) + (v00 + x0) / W] = __uint_as_float((uint32_t)(127 - e) << 23);
         }
 #pragma unroll
         for (int g = 0; g < W / 8; ++g) {
@@ -738,21 +753,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
             const float o0 = __uint_as_float(o[8 * g + 2 * y]) * f, o1 = __uint_as_float(o[8 * g + 2 * y + 1]) * f;
             w[y] = p.nsplit > 1 ? pack_f16x2(o0, o1) : pack_bf16x2(o0, o1);
           }
-          *reinterpret_cast<uint4*>(dst + 16 * g) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(mine + x0 * 2 + 16 * g) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
       fence_proxy_async_smem();
-    }
-    bar_sync(2 + (quarter & 1), 128);
-    if (write && kg == 0 && c == 0) {
-      // this warp's rows, one a lane
       if (head_ok) {
-        void* dst = p.nsplit == 1 ? static_cast<void*>(p.out + (orow * p.H + h) * DV)
-                                  : static_cast<void*>(p.part_o + (orow * p.H + h) * DV);
-        bulk_store(dst, sKV + r * PITCH, DV * 2);
+        const size_t at = (orow * p.H + h) * DV + v00;
+        void* dst = p.nsplit == 1 ? static_cast<void*>(p.out + at) : static_cast<void*>(p.part_o + at);
+        bulk_store(dst, mine, TC * 2);
       }
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      __syncwarp();
     }
     if (ok && kg == 0 && c == 0 && head_ok) {
       const float lse2 = l > 0.f ? R + log2f(l) : -INFINITY;
