@@ -165,12 +165,6 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// asynchronous copy of `bytes` (a multiple of 16) from shared to global memory
-__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
-               : "memory");
-}
-
 // largest magnitude of eight BF16 numbers, as its bits
 __device__ __forceinline__ uint32_t max_abs8(const uint4& v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -713,9 +707,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
       ok = false;
     }
     // A thread has a quarter of one row in 16-byte pieces, which as stores of
-    // their own would touch 32 lines an instruction; it puts them side by side
-    // in the keys' regions (every MMA is done) and sends them out as bulk
-    // copies.  The pitch keeps the pieces of eight threads on different banks.
+    // their own would touch 32 lines an instruction: the warp's 32 quarters
+    // are turned in the keys' regions (every MMA is done) and leave as whole
+    // 128-byte lines.  The pitch keeps the pieces of eight threads on
+    // different banks.  (Bulk copies of the quarters, one a thread, took 2000
+    // cycles to issue.)
     constexpr int TC = C::OCOLS / 2;                     // value columns of a thread
     constexpr int PITCH = TC * 2 + 16;
     static_assert(256 * PITCH <= C::KV_BYTES, "output staging");
@@ -737,9 +733,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
         tmem_wait_ld_dep(o);
         float f = inv;
         if (p.nsplit > 1) {
-          float mo = 0.f;
+          float m4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < W; ++i) mo = fmaxf(mo, fabsf(__uint_as_float(o[i])));
+          for (int i = 0; i < W; ++i) m4[i & 3] = fmaxf(m4[i & 3], fabsf(__uint_as_float(o[i])));
+          const float mo = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           // the power of two that brings the group's largest into [2^14, 2^15)
           const int e = min(max(127 + 14 - (int)(__float_as_uint(mo * inv) >> 23), -120), 126);
           f = inv * __uint_as_float((uint32_t)(127 + e) << 23);
@@ -756,15 +753,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
           *reinterpret_cast<uint4*>(mine + x0 * 2 + 16 * g) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      fence_proxy_async_smem();
-      if (head_ok) {
-        const size_t at = (orow * p.H + h) * DV + v00;
-        void* dst = p.nsplit == 1 ? static_cast<void*>(p.out + at) : static_cast<void*>(p.part_o + at);
-        bulk_store(dst, mine, TC * 2);
-      }
-      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
       __syncwarp();
+      constexpr int LPR = TC * 2 / 16;                   // lanes of a quarter row
+      uint16_t* base = p.nsplit == 1 ? p.out : reinterpret_cast<uint16_t*>(p.part_o);
+      const int h0 = h - lane, lr = lane / LPR, lc = lane % LPR;
+#pragma unroll
+      for (int i = 0; i < LPR; ++i) {
+        const int rr = i * (32 / LPR) + lr;
+        const uint4 w = *reinterpret_cast<const uint4*>(sKV + (sw * 32 + rr) * PITCH + lc * 16);
+        if (h0 + rr < p.H) *reinterpret_cast<uint4*>(base + (orow * p.H + h0 + rr) * DV + v00 + lc * 8) = w;
+      }
     }
     if (ok && kg == 0 && c == 0 && head_ok) {
       const float lse2 = l > 0.f ? R + log2f(l) : -INFINITY;
