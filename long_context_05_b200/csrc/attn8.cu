@@ -293,7 +293,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     if (threadIdx.x == 0) report_error(p.err, DSA_ERR_DEVICE_BOUNDS, ERR_SITE_ATTN8 | (0xAu << 8));
     return;
   }
-  pdl_launch_dependents();                     // the combine may be scheduled; it waits for this grid
+  // what follows on the stream may be scheduled now (the combine, or another
+  // call's kernel: both wait for this grid before they touch memory), and this
+  // kernel waits for what was before it
+  pdl_launch_dependents();
+  pdl_wait();
   uint8_t* sQ = smem + C::OFF_Q;
   uint8_t* sKV = smem + C::OFF_KV;
   uint8_t* sP = smem + C::OFF_P;
@@ -783,51 +787,59 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
 }
 
 // Merge the key splits of each (row, head): weights 2^(lse_s - max).  A thread
-// takes four columns; the loads of up to eight splits are issued before the
-// first is used (one memory latency a batch).  128 threads of up to 80
-// registers fit beside an attention CTA, so that the blocks can wait there for its end.
+// takes eight columns of a head and the splits four at a time, with the
+// batch's loads issued before the first is used and a running maximum.  128
+// threads of up to 80 registers fit beside an attention CTA, so that the
+// blocks can wait there for its end.
 constexpr int kCombineThreads = 128;
 template <int DV>
 __global__ void __launch_bounds__(kCombineThreads, 6) attn8_combine_kernel(const __half* part_o, const float* part_f,
-                                                            const float* part_lse, uint16_t* out, float* lse,
-                                                            long long heads, int H, int nsplit) {
-  constexpr int kBatch = 8, TPH = DV / 4, W = DV >= 128 ? 32 : 16;
+                                                                           const float* part_lse, uint16_t* out,
+                                                                           float* lse, int heads, int H, int nsplit) {
+  constexpr int kBatch = 4, TPH = DV / 8, W = DV >= 128 ? 32 : 16;
   pdl_wait();
-  const long long gh = (long long)blockIdx.x * (kCombineThreads / TPH) + threadIdx.x / TPH;
+  const int gh = blockIdx.x * (kCombineThreads / TPH) + threadIdx.x / TPH;
   if (gh >= heads) return;
-  const long long row = gh / H;
-  const int h = (int)(gh - row * H), d0 = (threadIdx.x % TPH) * 4;
-  const long long first = row * nsplit * H + h;            // split s at + s H
-  float mx = -INFINITY;
-  if (nsplit > kBatch)
-    for (int s = 0; s < nsplit; ++s) mx = fmaxf(mx, part_lse[first + (long long)s * H]);
-  float acc[4] = {0.f, 0.f, 0.f, 0.f}, wsum = 0.f;
-  for (int s0 = 0; s0 < nsplit; s0 += kBatch) {
+  const int row = gh / H, d0 = (threadIdx.x % TPH) * 8;
+  // split s of this head lies at first + s H
+  const size_t first = (size_t)row * nsplit * H + (gh - row * H);
+  const float* pl = part_lse + first;
+  const float* pf = part_f + first * (DV / W) + d0 / W;
+  const __half* po = part_o + first * DV + d0;
+  float mx = -INFINITY, wsum = 0.f, acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  for (int s = nsplit; s > 0; s -= kBatch) {
     float l[kBatch], f[kBatch];
-    uint2 v[kBatch];
+    uint4 v[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const long long at = first + (long long)(s0 + i) * H;
       l[i] = -INFINITY;
-      if (s0 + i < nsplit) {
-        l[i] = part_lse[at];
-        v[i] = *reinterpret_cast<const uint2*>(part_o + at * DV + d0);
-        f[i] = part_f[at * (DV / W) + d0 / W];
+      if (i < s) {
+        l[i] = *pl;
+        f[i] = *pf;
+        v[i] = *reinterpret_cast<const uint4*>(po);
+        pl += H;
+        pf += H * (DV / W);
+        po += H * DV;
       }
     }
-    if (nsplit <= kBatch) {
+    const float m = fmaxf(mx, fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])));
+    if (m == -INFINITY) continue;
+    const float alpha = exp2f(mx - m);
+    mx = m;
+    wsum *= alpha;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) mx = fmaxf(mx, l[i]);
-    }
+    for (int i = 0; i < 8; ++i) acc[i] *= alpha;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       if (l[i] == -INFINITY) continue;                     // an empty part's output was never written
       const float w = exp2f(l[i] - mx);
       wsum += w;
       const float wf = w * f[i];
-      const uint32_t u[2] = {v[i].x, v[i].y};
+      const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < 4; ++c) {
         const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&u[c]));
         acc[2 * c] = fmaf(wf, x.x, acc[2 * c]);
         acc[2 * c + 1] = fmaf(wf, x.y, acc[2 * c + 1]);
@@ -835,8 +847,10 @@ __global__ void __launch_bounds__(kCombineThreads, 6) attn8_combine_kernel(const
     }
   }
   const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
-  *reinterpret_cast<uint2*>(out + gh * DV + d0) =
-      make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+  *reinterpret_cast<uint4*>(out + (size_t)gh * DV + d0) = make_uint4(w[0], w[1], w[2], w[3]);
   if (d0 == 0 && lse != nullptr) lse[gh] = wsum > 0.f ? (mx + log2f(wsum)) * 0.6931471805599453f : -INFINITY;
 }
 
@@ -846,13 +860,15 @@ cudaError_t launch_t(const LaunchCtx& c, const Params& p) {
   static std::atomic<int> granted[kMaxDevices];
   cudaError_t e = grant_smem(attn8_kernel<DK, DV, PAGED>, C::BYTES, c.device, granted);
   if (e != cudaSuccess) return e;
-  attn8_kernel<DK, DV, PAGED><<<(unsigned)((long long)p.rows * p.nsplit * p.hsplit), kThreads, C::BYTES, c.stream>>>(p);
+  e = launch_pdl(attn8_kernel<DK, DV, PAGED>, dim3((unsigned)((long long)p.rows * p.nsplit * p.hsplit)), dim3(kThreads),
+                 C::BYTES, c.stream, p);
+  if (e != cudaSuccess) return e;
   note_launches(1);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.nsplit == 1) return e;
   // a programmatic dependent: its blocks may start while the attention drains
-  const long long heads = (long long)p.rows * p.H;
-  const int per = kCombineThreads / (DV / 4);
+  const int heads = p.rows * p.H;
+  const int per = kCombineThreads / (DV / 8);
   e = launch_pdl(attn8_combine_kernel<DV>, dim3((unsigned)((heads + per - 1) / per)), dim3(kCombineThreads), 0, c.stream,
                  (const __half*)p.part_o, (const float*)p.part_f, (const float*)p.part_lse, p.out, p.lse, heads, p.H,
                  p.nsplit);

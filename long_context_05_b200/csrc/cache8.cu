@@ -18,7 +18,8 @@
 // 64 and 128 contiguous bytes per row and instruction), its maximum taken by
 // three shuffles.  One launch serves the attention rows, the indexer's keys
 // and the indexer's queries: a decode step appends a few KB, where a launch
-// costs more than the work.
+// costs more than the work.  The kernels are programmatic dependents of what
+// is before them on the stream, so that their launch overlaps its end.
 #include <cuda_fp8.h>
 
 #include "internal.h"
@@ -135,6 +136,8 @@ __device__ __forceinline__ long long new_row(const KvMap& map, int n, int T, Dev
 
 template <int VK, int VI, bool PAGED>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(WriteParams p) {
+  sm100::pdl_launch_dependents();
+  sm100::pdl_wait();
   const int gl = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
   int blk = blockIdx.x;
   if (blk < p.kv_blocks + p.kI_blocks) {
@@ -200,6 +203,8 @@ __device__ __forceinline__ void dequantise_row(const uint8_t* src, float scale, 
 
 template <int VK, int VI, bool PAGED>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(ReadParams p) {
+  sm100::pdl_launch_dependents();
+  sm100::pdl_wait();
   const int gl = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
   int blk = blockIdx.x;
   const bool keys = blk >= p.kv_blocks;
@@ -227,13 +232,15 @@ unsigned blocks_for(long long rows) { return (unsigned)((rows + kRows - 1) / kRo
 
 template <int VK, int VI, bool PAGED>
 cudaError_t write_t(const LaunchCtx& c, const WriteParams& p, unsigned blocks) {
-  cache_write_kernel<VK, VI, PAGED><<<blocks, kThreads, 0, c.stream>>>(p);
+  const cudaError_t e = launch_pdl(cache_write_kernel<VK, VI, PAGED>, dim3(blocks), dim3(kThreads), 0, c.stream, p);
+  if (e != cudaSuccess) return e;
   note_launches(1);
   return cudaGetLastError();
 }
 template <int VK, int VI, bool PAGED>
 cudaError_t read_t(const LaunchCtx& c, const ReadParams& p, unsigned blocks) {
-  cache_read_kernel<VK, VI, PAGED><<<blocks, kThreads, 0, c.stream>>>(p);
+  const cudaError_t e = launch_pdl(cache_read_kernel<VK, VI, PAGED>, dim3(blocks), dim3(kThreads), 0, c.stream, p);
+  if (e != cudaSuccess) return e;
   note_launches(1);
   return cudaGetLastError();
 }

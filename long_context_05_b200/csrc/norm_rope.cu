@@ -203,9 +203,13 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(V, BACK)) norm_rope_ke
     bulk_load(d, (BACK ? s.dy : s.x) + at, bytes, &full[st]);
     if (BACK && need_x) bulk_load(d + p.tensor_bytes, s.x + at, bytes, &full[st]);
   };
+  pdl_launch_dependents();
   if (lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
     fence_mbar_init();
+  }
+  pdl_wait();                                     // nothing of global memory is read before this
+  if (lane == 0) {
     for (int i = tile0; i < tile1 && i < tile0 + kStages; ++i) load_tile(i);
   }
   __syncwarp();
@@ -451,6 +455,8 @@ struct DwParams {
 __global__ void __launch_bounds__(256) norm_rope_dw_kernel(DwParams p) {
   __shared__ float red[32][9];
   const int sd = blockIdx.y;
+  pdl_launch_dependents();
+  pdl_wait();
   if (p.dw[sd] == nullptr) return;
   const int c = blockIdx.x * 8 + (threadIdx.x & 7), l = threadIdx.x >> 3;
   float a = 0.f;
@@ -529,7 +535,9 @@ cudaError_t launch_mode(const LaunchCtx& c, const NrParams& p, size_t smem) {
   static std::atomic<int> granted[kMaxDevices];
   const cudaError_t e = grant_smem(kern, (int)smem, c.device, granted);
   if (e != cudaSuccess) return e;
-  kern<<<p.side[0].blocks + p.side[1].blocks, kThreads, smem, c.stream>>>(p);
+  const cudaError_t l = launch_pdl(kern, dim3((unsigned)(p.side[0].blocks + p.side[1].blocks)), dim3(kThreads), smem,
+                                   c.stream, p);
+  if (l != cudaSuccess) return l;
   note_launches(1);
   return cudaGetLastError();
 }
@@ -658,7 +666,8 @@ extern "C" dsa_status dsa_norm_rope_backward(const dsa_shape* s, const dsa_norm_
   }
   if (launch_nr(c, p, d, true) != cudaSuccess) return DSA_ERR_CUDA;
   if (w.dw[0] != nullptr || w.dw[1] != nullptr) {
-    norm_rope_dw_kernel<<<dim3((p.norm + 7) / 8, 2), 256, 0, c.stream>>>(w);
+    if (launch_pdl(norm_rope_dw_kernel, dim3((unsigned)((p.norm + 7) / 8), 2), dim3(256), 0, c.stream, w) != cudaSuccess)
+      return DSA_ERR_CUDA;
     note_launches(1);
     if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
   }
