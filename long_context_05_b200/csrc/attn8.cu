@@ -87,7 +87,7 @@ struct Cfg {
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_KV = (2 * QPIECE + 1023) / 1024 * 1024;
   static constexpr int OFF_P = OFF_KV + KV_BYTES;      // [2][hi, lo][64 rows x 128 bytes]
-  static constexpr int OFF_PAR = OFF_P + 4 * PTERM;    // [2][128] {a s, log2 s}, [2][128] 1 / s
+  static constexpr int OFF_PAR = OFF_P + 4 * PTERM;    // [2][3][128]: a s, log2 s, 1 / s of the keys
   static constexpr int OFF_MX = OFF_PAR + 2 * kN * 12; // [2][4][64] partial maxima
   static constexpr int OFF_E = OFF_MX + 2 * 4 * kM * 4;  // [64] 2^e of the head rows
   static constexpr int OFF_BAR = OFF_E + kM * 4;
@@ -159,6 +159,43 @@ __device__ __forceinline__ void mma_ws_ts(uint32_t d_tmem, uint32_t a_tmem, uint
       "tcgen05.mma.ws.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// two FP32 numbers an instruction
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair2u(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 __device__ __forceinline__ void bar_sync(int id, int threads) {
@@ -301,8 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
   uint8_t* sQ = smem + C::OFF_Q;
   uint8_t* sKV = smem + C::OFF_KV;
   uint8_t* sP = smem + C::OFF_P;
-  float2* sPar = reinterpret_cast<float2*>(smem + C::OFF_PAR);        // [2][128]
-  float* sInv = reinterpret_cast<float*>(smem + C::OFF_PAR + 2 * kN * 8);
+  float* sPar = reinterpret_cast<float*>(smem + C::OFF_PAR);
   float* sMx = reinterpret_cast<float*>(smem + C::OFF_MX);
   float* sE = reinterpret_cast<float*>(smem + C::OFF_E);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -480,8 +516,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
       for (int u = 0; u < 4; ++u) {
         const float s = s_cur[u];
         const bool on = s > 0.f;
-        sPar[pb * kN + lane + 32 * u] = make_float2(p.scale_log2 * s, on ? log2f(s) : -INFINITY);
-        sInv[pb * kN + lane + 32 * u] = on ? 1.f / s : 0.f;
+        float* par = sPar + pb * 3 * kN + lane + 32 * u;
+        par[0] = p.scale_log2 * s;
+        par[kN] = on ? log2f(s) : -INFINITY;
+        par[2 * kN] = on ? 1.f / s : 0.f;
         s_cur[u] = s_next[u];
       }
       mbar_arrive(&par_full[pb]);
@@ -627,17 +665,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
       uint32_t s[32];
       tmem_ld32(tmem + lane_addr + C::SCOL + pb * (kN / 2) + c * 32, s);
       tmem_wait_ld_dep(s);
-      const int key0 = pb * kN + kg * 64 + c * 32;
-      const float4* par = reinterpret_cast<const float4*>(sPar + key0);
+      // (two keys an instruction where FP32 comes packed)
+      const ulonglong2* par = reinterpret_cast<const ulonglong2*>(sPar + pb * 3 * kN + kg * 64 + c * 32);
+      const uint64_t f2 = pair2(f_h, f_h);
+      uint64_t x[16];
       float cm = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float4 a = par[i];
-        const float x0 = fmaf(__uint_as_float(s[2 * i]) * f_h, a.x, a.y);
-        const float x1 = fmaf(__uint_as_float(s[2 * i + 1]) * f_h, a.z, a.w);
-        s[2 * i] = __float_as_uint(x0);
-        s[2 * i + 1] = __float_as_uint(x1);
-        cm = fmaxf(cm, fmaxf(x0, x1));
+      for (int i = 0; i < 8; ++i) {
+        const ulonglong2 a = par[i], lg = par[kN / 4 + i];
+        x[2 * i] = fma2(mul2(pair2u(s[4 * i], s[4 * i + 1]), f2), a.x, lg.x);
+        x[2 * i + 1] = fma2(mul2(pair2u(s[4 * i + 2], s[4 * i + 3]), f2), a.y, lg.y);
+        const float2 x0 = unpair2(x[2 * i]), x1 = unpair2(x[2 * i + 1]);
+        cm = max3(cm, x0.x, x0.y);
+        cm = max3(cm, x1.x, x1.y);
       }
       // 2. the row's maximum over its four threads, and the reference
       float* mx = sMx + pb * 4 * kM + r;
@@ -657,22 +697,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
       // 3. P in two terms, to shared memory (free: the q K^T of this chunk
       //    came after the P V that read the buffer)
       const float nR = R == -INFINITY ? 0.f : -R;
-      const float4* inv = reinterpret_cast<const float4*>(sInv + key0);
+      const uint64_t nR2 = pair2(nR, nR);
+      const ulonglong2* inv = par + 2 * kN / 4;
       uint8_t* prow = sP + pb * 2 * C::PTERM + r * 128;
-      float rs0 = 0.f, rs1 = 0.f;
+      uint64_t rs0 = 0ull, rs1 = 0ull;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         uint32_t hw[4], lw[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float4 iv = inv[4 * g + i];
-          const int k0 = 16 * g + 4 * i;
-          const float e0 = ex2_approx(__uint_as_float(s[k0]) + nR), e1 = ex2_approx(__uint_as_float(s[k0 + 1]) + nR);
-          const float e2 = ex2_approx(__uint_as_float(s[k0 + 2]) + nR), e3 = ex2_approx(__uint_as_float(s[k0 + 3]) + nR);
-          rs0 = fmaf(e0, iv.x, rs0);
-          rs1 = fmaf(e1, iv.y, rs1);
-          rs0 = fmaf(e2, iv.z, rs0);
-          rs1 = fmaf(e3, iv.w, rs1);
+          const ulonglong2 iv = inv[4 * g + i];
+          const float2 y0 = unpair2(add2(x[8 * g + 2 * i], nR2)), y1 = unpair2(add2(x[8 * g + 2 * i + 1], nR2));
+          const float e0 = ex2_approx(y0.x), e1 = ex2_approx(y0.y), e2 = ex2_approx(y1.x), e3 = ex2_approx(y1.y);
+          rs0 = fma2(pair2(e0, e1), iv.x, rs0);
+          rs1 = fma2(pair2(e2, e3), iv.y, rs1);
           uint32_t h0, l0, h1, l1;
           split2(e0, e1, h0, l0);
           split2(e2, e3, h1, l1);
@@ -683,7 +721,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
         *reinterpret_cast<uint4*>(d) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
         *reinterpret_cast<uint4*>(d + C::PTERM) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
       }
-      l += rs0 + rs1;
+      const float2 rs = unpair2(add2(rs0, rs1));
+      l += rs.x + rs.y;
       fence_proxy_async_smem();
       // 4. the accumulator follows the reference, once the P V before this
       //    chunk is done (that of an even chunk's predecessor is: its q K^T
