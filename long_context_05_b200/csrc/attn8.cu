@@ -143,22 +143,43 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
 }
 
 // D[tmem] (+)= A B^T, e4m3, the M = 64 form that uses all lanes; A in shared
-// memory or in TMEM (in lanes 0-63 and again in 64-127)
-__device__ __forceinline__ void mma_ws(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+// memory or in TMEM (in lanes 0-63 and again in 64-127).  The two terms of A
+// meet the same B one after the other: the first MMA leaves B in the
+// collector and the second takes it from there, which halves the reads of
+// shared memory, the bound of this kernel.
+template <int TERM>
+__device__ __forceinline__ void mma_ws(uint32_t d_tmem, uint64_t a, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.ws.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+  if constexpr (TERM == 0) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.ws.cta_group::1.kind::f8f6f4.collector::b0::fill [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.ws.cta_group::1.kind::f8f6f4.collector::b0::lastuse [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
 }
-__device__ __forceinline__ void mma_ws_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+template <int TERM>
+__device__ __forceinline__ void mma_ws_ts(uint32_t d_tmem, uint32_t a, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.ws.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+  if constexpr (TERM == 0) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.ws.cta_group::1.kind::f8f6f4.collector::b0::fill [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.ws.cta_group::1.kind::f8f6f4.collector::b0::lastuse [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
 }
 
 // two FP32 numbers an instruction
@@ -553,25 +574,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
           const uint64_t ktl = ktail0 + (uint64_t)((rg * kN * 64) >> 4);
           const uint32_t dS = tmem + C::SCOL + rg * (kN / 2);
 #pragma unroll
-          for (int ks = 0; ks < C::KSTEPS; ++ks)
-#pragma unroll
-            for (int term = 0; term < 2; ++term) {
-              const int d = ks * 32;
-              const uint32_t acc = (term > 0 || ks > 0) ? 1u : 0u;
-              if (d < C::NF * 128) {
-                const uint64_t bdesc = kst + (uint64_t)(((d / 128) * C::ATOM + (d % 128)) >> 4);
-                if (d < C::QT) {
-                  mma_ws_ts(dS, tmem + C::QCOL + term * (C::QT / 4) + d / 4, bdesc, idesc_qk, acc);
-                } else {
-                  const int dq = d - C::QT;
-                  mma_ws(dS, qdesc0 + (uint64_t)((term * C::QPIECE + (dq / 128) * (kM * 128) + (dq % 128)) >> 4), bdesc,
-                         idesc_qk, acc);
-                }
+          for (int ks = 0; ks < C::KSTEPS; ++ks) {
+            const int d = ks * 32;
+            const uint32_t acc = ks > 0 ? 1u : 0u;
+            if (d < C::NF * 128) {
+              const uint64_t bdesc = kst + (uint64_t)(((d / 128) * C::ATOM + (d % 128)) >> 4);
+              if (d < C::QT) {
+                mma_ws_ts<0>(dS, tmem + C::QCOL + d / 4, bdesc, idesc_qk, acc);
+                mma_ws_ts<1>(dS, tmem + C::QCOL + C::QT / 4 + d / 4, bdesc, idesc_qk, 1u);
               } else {
-                const int dt = d - C::NF * 128;
-                mma_ws(dS, qtail0 + (uint64_t)((term * C::QPIECE + dt) >> 4), ktl + (uint64_t)(dt >> 4), idesc_qk, acc);
+                const int dq = d - C::QT;
+                const uint64_t adesc = qdesc0 + (uint64_t)(((dq / 128) * (kM * 128) + (dq % 128)) >> 4);
+                mma_ws<0>(dS, adesc, bdesc, idesc_qk, acc);
+                mma_ws<1>(dS, adesc + (uint64_t)(C::QPIECE >> 4), bdesc, idesc_qk, 1u);
               }
+            } else {
+              const int dt = d - C::NF * 128;
+              mma_ws<0>(dS, qtail0 + (uint64_t)(dt >> 4), ktl + (uint64_t)(dt >> 4), idesc_qk, acc);
+              mma_ws<1>(dS, qtail0 + (uint64_t)((C::QPIECE + dt) >> 4), ktl + (uint64_t)(dt >> 4), idesc_qk, 1u);
             }
+          }
           mma_commit(&s_full[rg]);
         }
         __syncwarp();
@@ -588,12 +610,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
 #pragma unroll
           for (int ks = 0; ks < kN / 32; ++ks) {
 #pragma unroll
-            for (int nv = 0; nv < C::NMMV; ++nv)
-#pragma unroll
-              for (int term = 0; term < 2; ++term)
-                mma_ws(tmem + C::OCOL + nv * (C::NV / 2), pst + (uint64_t)((term * C::PTERM + ks * 32) >> 4),
-                       vst + (uint64_t)((nv * (C::NV / 128) * C::ATOM + ks * 32 * 128) >> 4), idesc_pv,
-                       (pv > 0 || ks > 0 || term > 0) ? 1u : 0u);
+            for (int nv = 0; nv < C::NMMV; ++nv) {
+              const uint64_t bdesc = vst + (uint64_t)((nv * (C::NV / 128) * C::ATOM + ks * 32 * 128) >> 4);
+              const uint32_t dO = tmem + C::OCOL + nv * (C::NV / 2);
+              mma_ws<0>(dO, pst + (uint64_t)((ks * 32) >> 4), bdesc, idesc_pv, (pv > 0 || ks > 0) ? 1u : 0u);
+              mma_ws<1>(dO, pst + (uint64_t)((C::PTERM + ks * 32) >> 4), bdesc, idesc_pv, 1u);
+            }
             if (ks & 1) mma_commit(&kv_empty[2 * rg + ks / 2]);
           }
         }
