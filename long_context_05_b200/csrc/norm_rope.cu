@@ -243,13 +243,16 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(V, BACK)) norm_rope_ke
   }
   const AbortSources no_abort{nullptr, nullptr};
   int n_lo = 0, n_cnt = 0;                        // tokens whose angles cs holds
+  // the tile's first row is head `off` of token n0; small numbers are divided
+  // by H through its reciprocal (both below 2^11: exact, with the half)
+  auto by_H = [&](int x) { return (int)(((float)x + 0.5f) * s.inv_H); };
+  int n0 = tile0 * p.rt / s.H, off = tile0 * p.rt - n0 * s.H;
   bool ok = true;
   for (int tile = tile0; tile < tile1; ++tile) {
     const int st = (tile - tile0) % kStages;
     const int row0 = tile * p.rt, nr = min(p.rt, s.rows - row0);
-    const int n0 = row0 / s.H, off = row0 - n0 * s.H;
     if (MODE != kNone) {
-      const int nt = (off + nr - 1) / s.H + 1;
+      const int nt = by_H(off + nr - 1) + 1;
       if (n0 < n_lo || n0 + nt > n_lo + n_cnt) {
         fill_angles(p, cs, n0, nt);
         n_lo = n0;
@@ -257,9 +260,13 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(V, BACK)) norm_rope_ke
         __syncwarp();
       }
     }
-    if (ok && !mbar_wait(&full[st], (uint32_t)((tile - tile0) / kStages) & 1, p.wait_ns, no_abort)) {
-      report_error(p.err, DSA_ERR_TIMEOUT, ERR_SITE_NORM | (2u << 8));
-      ok = false;
+    ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (uint32_t)((tile - tile0) / kStages) & 1, p.wait_ns, no_abort));
+    if (!ok) {
+      if (lane == 0) report_error(p.err, DSA_ERR_TIMEOUT, ERR_SITE_NORM | (2u << 8));
+      // the copies still on their way, with the same limit
+      for (int i = tile + 1; i < tile1 && i < tile + kStages; ++i)
+        mbar_wait(&full[(i - tile0) % kStages], (uint32_t)((i - tile0) / kStages) & 1, p.wait_ns, no_abort);
+      break;
     }
     const uint8_t* sA = ring + st * kTensors * p.tensor_bytes;     // x forward, dy backward
     for (int rr = 0; rr < nr; rr += GP * U) {
@@ -272,11 +279,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(V, BACK)) norm_rope_ke
         ra[u] = reinterpret_cast<const uint4*>(sA + r[u] * p.D * 2) + gl;
         ss2[u] = dot2[u] = 0ull;
       }
-      // the angles of row r: its token within those of cs ((off + r) / H by
-      // the reciprocal: both below 2^11, exact with the half)
-      auto angles = [&](int r_) -> const float2* {
-        return cs + (n0 - n_lo + (int)(((float)(off + r_) + 0.5f) * s.inv_H)) * half;
-      };
+      // the angles of row r: its token within those of cs
+      auto angles = [&](int r_) -> const float2* { return cs + (n0 - n_lo + by_H(off + r_)) * half; };
       // columns `col` of the partner range (col rotated)
       auto partner = [&](int u, int col) -> F8 {
         const int pc = col - r0 < half ? col + half : col - half;
@@ -360,7 +364,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(V, BACK)) norm_rope_ke
         }
         return o;
       };
-      auto live = [&](int u) { return ok && rr + u * GP + grp < nr; };
+      const bool whole = rr + GP * U <= nr;        // the same for the warp
+      auto live = [&](int u) { return whole || rr + u * GP + grp < nr; };
       // 2. the rows out
 #pragma unroll
       for (int j = 0; j < V; ++j) {
@@ -416,7 +421,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(V, BACK)) norm_rope_ke
       }
     }
     __syncwarp();                                 // the stage is read
-    if (lane == 0 && ok && tile + kStages < tile1) load_tile(tile + kStages);
+    if (lane == 0 && tile + kStages < tile1) load_tile(tile + kStages);
+    const int q = by_H(off + p.rt);
+    n0 += q;
+    off += p.rt - q * s.H;
   }
   if constexpr (BACK) {
     if (s.dw_part == nullptr) return;
