@@ -454,12 +454,14 @@ DSA_API size_t dsa_workspace8_size(const dsa_shape* shape);
  * anything.  The products are those of the given bytes with q split into two
  * e4m3 terms and of the probabilities split likewise, accumulated in FP32;
  * out is rounded to BF16 once.  The two modes give the same results; calls of
- * few rows split their keys over the SMs and need the workspace. */
+ * few rows split their keys over the SMs and need the workspace.  B T H is
+ * below 2^31. */
 DSA_API dsa_status dsa_sparse_attn8(const dsa_shape* shape, const uint16_t* q, const uint8_t* kv8,
                             const float* kv_scale, const int32_t* idx, uint16_t* out, float* lse, void* ws,
                             size_t ws_bytes, void* stream);
 
-/* dsa_dense_attn over an 8-bit cache: every query over all its visible keys. */
+/* dsa_dense_attn over an 8-bit cache: every query over all its visible keys
+ * (the rows of all L_b keys of a sequence hold no NaN bytes). */
 DSA_API dsa_status dsa_dense_attn8(const dsa_shape* shape, const uint16_t* q, const uint8_t* kv8,
                            const float* kv_scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
                            void* stream);

@@ -24,16 +24,20 @@
 //     is then 2^-14 of it or less.
 // Logits, P before its rounding, l and the output accumulate in FP32.
 //
-// Work split.  A CTA takes 64 heads of one query (all of them when there are
-// no more) and all value columns, as the M = 64 of tcgen05.mma.ws: that form
+// Work split.  A CTA takes 64 head rows and all value columns: heads of one
+// query, or in a dense call, where the queries of a sequence share their keys,
+// rows of the sequence's T x H (several queries where there are few heads,
+// with the keys past a row's own position masked in its logits; 1538 dense
+// queries over up to 1537 keys: 225 -> 50 us at 8 heads, 480 -> 292 at 72,
+// no change at 64 and 128).  They are the M = 64 of tcgen05.mma.ws: that form
 // spreads a 64 x N result over all 128 TMEM lanes (lanes 0-63 the first N/2
 // columns, 64-127 the rest), so the 64 x 512 FP32 accumulator takes half of
 // TMEM.  With M = 128 it would fill TMEM, and the way out, a CTA per half of
 // the value columns, computes every logit twice.  Measured, back to back:
 // N = 128 45-49 cycles, N = 256 77-82 (M = 128: 64 and 129), so a query's
-// 128 keys cost 2 x 3000 cycles in place of 2 x 4400 (M = 128 with the N = 64
-// that fits beside the accumulator).  Few queries also split their keys, and a
-// combine kernel merges the parts.
+// 128 keys cost 2 x 3000 cycles of MMAs in place of 2 x 4400 (M = 128 with the
+// N = 64 that fits beside the accumulator).  Few head rows also split their
+// keys, and a combine kernel merges the parts.
 //
 // Per CTA: TMEM holds O (256 columns) | two S buffers of 64 | q_hi and q_lo of
 // the first 256 key columns, in both lane halves.  Shared memory holds the
@@ -118,7 +122,9 @@ struct Params {
   float* part_f;         // [rows, nsplit, H, d_v / 32 (16)]
   float* part_lse;       // [rows, nsplit, H], log2 units
   int T, H, k;
-  int rows, nsplit, hsplit;
+  // A unit is one query, with its H head rows, or in a dense call one
+  // sequence, with all its T H; a CTA takes 64 head rows of one.
+  int units, HR, nsplit, hsplit;
   float scale_log2;      // tau log2(e)
   long long wait_ns;
   DevErr* err;
@@ -375,20 +381,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int hs = blockIdx.x % p.hsplit;        // heads [64 hs, 64 hs + 64)
+  const bool packed = p.idx == nullptr;        // units are sequences
+  const int hs = blockIdx.x % p.hsplit;        // head rows [64 hs, 64 hs + 64) of the unit
   const int rest = blockIdx.x / p.hsplit;
-  const int row = rest / p.nsplit;             // b * T + t
-  const int split = rest - row * p.nsplit;
-  const int b = row / p.T, t = row - b * p.T;
+  const int unit = rest / p.nsplit;            // b * T + t, or b
+  const int split = rest - unit * p.nsplit;
+  const int b = packed ? unit : unit / p.T;
+  const int nrows = min(kM, p.HR - hs * kM);
+  const int t = packed ? (hs * kM + nrows - 1) / p.H : unit - b * p.T;   // the last query of the rows
   const int Lb = p.map.len(b, threadIdx.x == 0 ? p.err : nullptr, ERR_SITE_ATTN8);
-  const bool dense = p.idx == nullptr || t < p.dense_rows;
-  const int nslots = dense ? Lb - p.T + t + 1 : p.k;      // slots of this row
+  const bool dense = packed || t < p.dense_rows;
+  const int nslots = dense ? Lb - p.T + t + 1 : p.k;      // slots of these rows
   // an equal share of the row's chunks for every split
   const int kc = ((nslots + kN - 1) / kN + p.nsplit - 1) / p.nsplit * kN;
   const int slot0 = min(split * kc, nslots), slot1 = min(slot0 + kc, nslots);
   const int nchunks = (slot1 - slot0 + kN - 1) / kN;
 
-  const int32_t* irow = dense ? nullptr : p.idx + (size_t)row * p.k;
+  const int32_t* irow = dense ? nullptr : p.idx + (size_t)unit * p.k;
   // index of slot s of this split; -1 past the end and for an empty slot
   auto load_idx = [&](int s) -> int { return s < slot1 ? (dense ? s : irow[s]) : -1; };
   // q's rows are on their way while the barriers and TMEM are set up: the
@@ -402,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
   }
   QRows<DK> q4;
   if (warp >= kFirstSoftmax)
-    load_q_rows(q4, p.q + ((size_t)row * p.H + hs * kM) * DK, p.H - hs * kM, warp - kFirstSoftmax, lane);
+    load_q_rows(q4, p.q + ((size_t)unit * p.HR + hs * kM) * DK, nrows, warp - kFirstSoftmax, lane);
 
   if (threadIdx.x == 0) {
     mbar_init(q_ready, 8);
@@ -508,11 +517,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     auto scale_of = [&](int r) -> float { return r < 0 ? 0.f : __ldg(p.kv_scale + base_row + r); };
     auto checked_row = [&](int v) -> int {
       if (v >= Lb) {
-        if (hs == 0) report_error(p.err, DSA_ERR_DEVICE_BOUNDS, ERR_SITE_ATTN8);
+        report_error(p.err, DSA_ERR_DEVICE_BOUNDS, ERR_SITE_ATTN8);
         return -1;
       }
       const int r = row_of(v);
-      if (PAGED && v >= 0 && r < 0 && hs == 0) report_error(p.err, DSA_ERR_DEVICE_BOUNDS, ERR_SITE_ATTN8 | (1u << 8));
+      if (PAGED && v >= 0 && r < 0) report_error(p.err, DSA_ERR_DEVICE_BOUNDS, ERR_SITE_ATTN8 | (1u << 8));
       return r;
     };
     int ip[4];
@@ -645,8 +654,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     const int quarter = warp & 3, c = sw >> 2;
     const int r = (quarter & 1) * 32 + lane, kg = quarter >> 1;
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
-    const int h = hs * kM + r;
-    const bool head_ok = h < p.H;
+    const int h = hs * kM + r;                           // head row of the unit
+    const bool head_ok = r < nrows;
+    // in a dense call the rows may be of several queries: this row's sees
+    // slots up to `last`
+    const int last = packed ? Lb - p.T + h / p.H : 0x7fffffff;
     float f_h = 0.f;
     split_q_rows<DK, DV>(q4, sw, lane, sQ, sP, sE);
     fence_proxy_async_smem();
@@ -697,6 +709,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
         const ulonglong2 a = par[i], lg = par[kN / 4 + i];
         x[2 * i] = fma2(mul2(pair2u(s[4 * i], s[4 * i + 1]), f2), a.x, lg.x);
         x[2 * i + 1] = fma2(mul2(pair2u(s[4 * i + 2], s[4 * i + 3]), f2), a.y, lg.y);
+      }
+      const int past = last - (slot0 + j * kN + kg * 64 + c * 32);   // keys i > past are not this row's
+      if (__any_sync(0xffffffffu, past < 31)) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 y = unpair2(x[i]);
+          x[i] = pair2(2 * i > past ? -INFINITY : y.x, 2 * i + 1 > past ? -INFINITY : y.y);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
         const float2 x0 = unpair2(x[2 * i]), x1 = unpair2(x[2 * i + 1]);
         cm = max3(cm, x0.x, x0.y);
         cm = max3(cm, x1.x, x1.y);
@@ -780,7 +803,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     constexpr int TC = C::OCOLS / 2;                     // value columns of a thread
     constexpr int PITCH = TC * 2 + 16;
     static_assert(256 * PITCH <= C::KV_BYTES, "output staging");
-    const size_t orow = p.nsplit == 1 ? (size_t)row : (size_t)row * p.nsplit + split;
+    // first head row of the unit (and split) in the output or the parts
+    const size_t orow = (p.nsplit == 1 ? (size_t)unit : (size_t)unit * p.nsplit + split) * p.HR;
     if (ok && nchunks > 0) {
       tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -805,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
           // the power of two that brings the group's largest into [2^14, 2^15)
           const int e = min(max(127 + 14 - (int)(__float_as_uint(mo * inv) >> 23), -120), 126);
           f = inv * __uint_as_float((uint32_t)(127 + e) << 23);
-          if (head_ok) p.part_f[(orow * p.H + h) * (DV / W) + (v00 + x0) / W] = __uint_as_float((uint32_t)(127 - e) << 23);
+          if (head_ok) p.part_f[(orow + h) * (DV / W) + (v00 + x0) / W] = __uint_as_float((uint32_t)(127 - e) << 23);
         }
 #pragma unroll
         for (int g = 0; g < W / 8; ++g) {
@@ -821,20 +845,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
       __syncwarp();
       constexpr int LPR = TC * 2 / 16;                   // lanes of a quarter row
       uint16_t* base = p.nsplit == 1 ? p.out : reinterpret_cast<uint16_t*>(p.part_o);
-      const int h0 = h - lane, lr = lane / LPR, lc = lane % LPR;
+      const int r0 = r - lane, lr = lane / LPR, lc = lane % LPR;
 #pragma unroll
       for (int i = 0; i < LPR; ++i) {
         const int rr = i * (32 / LPR) + lr;
         const uint4 w = *reinterpret_cast<const uint4*>(sKV + (sw * 32 + rr) * PITCH + lc * 16);
-        if (h0 + rr < p.H) *reinterpret_cast<uint4*>(base + (orow * p.H + h0 + rr) * DV + v00 + lc * 8) = w;
+        if (r0 + rr < nrows) *reinterpret_cast<uint4*>(base + (orow + hs * kM + r0 + rr) * DV + v00 + lc * 8) = w;
       }
     }
     if (ok && kg == 0 && c == 0 && head_ok) {
       const float lse2 = l > 0.f ? R + log2f(l) : -INFINITY;
       if (p.nsplit == 1) {
-        if (p.lse != nullptr) p.lse[orow * p.H + h] = lse2 * 0.6931471805599453f;
+        if (p.lse != nullptr) p.lse[orow + h] = lse2 * 0.6931471805599453f;
       } else {
-        p.part_lse[orow * p.H + h] = lse2;
+        p.part_lse[orow + h] = lse2;
       }
     }
   }
@@ -847,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
   }
 }
 
-// Merge the key splits of each (row, head): weights 2^(lse_s - max).  A thread
+// Merge the key splits of each head row (H rows to a unit): weights 2^(lse_s - max).  A thread
 // takes eight columns of a head and the splits four at a time, with the
 // batch's loads issued before the first is used and a running maximum.  128
 // threads of up to 80 registers fit beside an attention CTA, so that the
@@ -921,44 +945,51 @@ cudaError_t launch_t(const LaunchCtx& c, const Params& p) {
   static std::atomic<int> granted[kMaxDevices];
   cudaError_t e = grant_smem(attn8_kernel<DK, DV, PAGED>, C::BYTES, c.device, granted);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attn8_kernel<DK, DV, PAGED>, dim3((unsigned)((long long)p.rows * p.nsplit * p.hsplit)), dim3(kThreads),
+  e = launch_pdl(attn8_kernel<DK, DV, PAGED>, dim3((unsigned)((long long)p.units * p.nsplit * p.hsplit)), dim3(kThreads),
                  C::BYTES, c.stream, p);
   if (e != cudaSuccess) return e;
   note_launches(1);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.nsplit == 1) return e;
   // a programmatic dependent: its blocks may start while the attention drains
-  const int heads = p.rows * p.H;
+  const int heads = p.units * p.HR;
   const int per = kCombineThreads / (DV / 8);
   e = launch_pdl(attn8_combine_kernel<DV>, dim3((unsigned)((heads + per - 1) / per)), dim3(kCombineThreads), 0, c.stream,
-                 (const __half*)p.part_o, (const float*)p.part_f, (const float*)p.part_lse, p.out, p.lse, heads, p.H,
+                 (const __half*)p.part_o, (const float*)p.part_f, (const float*)p.part_lse, p.out, p.lse, heads, p.HR,
                  p.nsplit);
   note_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Key splits per query row: one wave of CTAs (one per SM) when there are
-// fewer rows than SMs, never less than one chunk to a split.
-int choose_nsplit(long long rows, int H, long long slots, int num_sms) {
-  const long long ctas = rows * ((H + kM - 1) / kM);
-  const long long chunks = (slots + kN - 1) / kN;
+// Units of a call, the CTAs that share one's head rows, and its key splits:
+// one wave of CTAs (one per SM) when there are fewer than SMs, never less than
+// one chunk to a split.
+struct Plan {
+  long long units;
+  int HR, hsplit, nsplit;
+};
+Plan plan(const Attn8Args& a, bool dense, int num_sms) {
+  Plan p;
+  p.units = dense ? a.B : (long long)a.B * a.T;
+  p.HR = dense ? a.T * a.H : a.H;
+  p.hsplit = (p.HR + kM - 1) / kM;
+  const long long ctas = p.units * p.hsplit, chunks = ((dense ? a.S : a.k) + kN - 1) / kN;
   long long n = num_sms / ctas;
   if (n < 1) n = 1;
-  return (int)(n < chunks ? n : chunks);
+  p.nsplit = (int)(n < chunks ? n : chunks);
+  return p;
 }
 
 // FP16 outputs, their factors (at most d_v / 16 a head) and log2-sum-exps
-size_t part_bytes(long long rows, int H, int d_v, int nsplit) {
-  return nsplit > 1 ? (size_t)rows * nsplit * H * (d_v * 2 + d_v / 16 * 4 + 4) : 0;
+size_t part_bytes(const Plan& p, int d_v) {
+  return p.nsplit > 1 ? (size_t)p.units * p.nsplit * p.HR * (d_v * 2 + d_v / 16 * 4 + 4) : 0;
 }
 
 }  // namespace
 
 // Workspace of the attention over an 8-bit cache, for sparse and dense calls.
 size_t attn8_workspace_bytes(const Attn8Args& a, int num_sms) {
-  const long long rows = (long long)a.B * a.T;
-  const size_t s = part_bytes(rows, a.H, a.d_v, choose_nsplit(rows, a.H, a.k, num_sms));
-  const size_t d = part_bytes(rows, a.H, a.d_v, choose_nsplit(rows, a.H, a.S, num_sms));
+  const size_t s = part_bytes(plan(a, false, num_sms), a.d_v), d = part_bytes(plan(a, true, num_sms), a.d_v);
   return ((s > d ? s : d) + 255) / 256 * 256;
 }
 
@@ -975,16 +1006,17 @@ cudaError_t launch_attn8(const LaunchCtx& c, const Attn8Args& a) {
   p.T = a.T;
   p.H = a.H;
   p.k = a.k;
-  const long long rows = (long long)a.B * a.T;
-  p.rows = (int)rows;
-  p.nsplit = choose_nsplit(rows, a.H, a.idx != nullptr ? a.k : a.S, c.num_sms);
-  p.hsplit = (a.H + kM - 1) / kM;
+  const Plan pl = plan(a, a.idx == nullptr, c.num_sms);
+  p.units = (int)pl.units;
+  p.HR = pl.HR;
+  p.hsplit = pl.hsplit;
+  p.nsplit = pl.nsplit;
   p.scale_log2 = a.tau * 1.4426950408889634f;
   p.wait_ns = c.wait_ns;
   p.err = c.err;
   if (p.nsplit > 1) {
     if (a.ws == nullptr) return cudaErrorInvalidValue;
-    const size_t n = (size_t)rows * p.nsplit * a.H;
+    const size_t n = (size_t)pl.units * p.nsplit * p.HR;
     p.part_o = static_cast<__half*>(a.ws);
     p.part_f = reinterpret_cast<float*>(p.part_o + n * a.d_v);
     p.part_lse = p.part_f + n * (a.d_v / 16);

@@ -370,6 +370,9 @@ Attn8Args attn8_args(const dsa_shape* s) {
   return a;
 }
 
+// head rows of a call count as an int
+bool attn8_rows_ok(const dsa_shape* s) { return (long long)s->B * s->T * s->H < (1LL << 31); }
+
 dsa_status run_attn8(const LaunchCtx& c, const dsa_shape* s, const uint16_t* q, const uint8_t* kv8,
                      const float* kv_scale, const int32_t* idx, int dense_rows, uint16_t* out, float* lse, void* ws,
                      size_t ws_bytes) {
@@ -567,7 +570,7 @@ dsa_status dsa_decode(const dsa_shape* s, const dsa_inputs* in, uint16_t* out, f
 
 // Steps A and B in the score tile's workspace, the attention's own behind it.
 size_t dsa_workspace8_size(const dsa_shape* s) {
-  if (check_shape(s) != DSA_OK) return 0;
+  if (check_shape(s) != DSA_OK || !attn8_rows_ok(s)) return 0;
   DeviceInfo d;
   int dev = 0;
   int sms = 148;
@@ -579,6 +582,7 @@ dsa_status dsa_sparse_attn8(const dsa_shape* s, const uint16_t* q, const uint8_t
                             const int32_t* idx, uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
   dsa_status st = check_shape(s);
   if (st != DSA_OK) return st;
+  if (!attn8_rows_ok(s)) return DSA_ERR_UNSUPPORTED;
   if (!attn8_ptrs_ok(q, kv8, kv_scale, out, ws) || idx == nullptr) return DSA_ERR_INVALID_ARG;
   LaunchCtx c;
   if ((st = make_ctx(stream, &c)) != DSA_OK) return st;
@@ -589,6 +593,7 @@ dsa_status dsa_dense_attn8(const dsa_shape* s, const uint16_t* q, const uint8_t*
                            uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
   dsa_status st = check_shape(s);
   if (st != DSA_OK) return st;
+  if (!attn8_rows_ok(s)) return DSA_ERR_UNSUPPORTED;
   if (!attn8_ptrs_ok(q, kv8, kv_scale, out, ws)) return DSA_ERR_INVALID_ARG;
   LaunchCtx c;
   if ((st = make_ctx(stream, &c)) != DSA_OK) return st;
@@ -599,6 +604,7 @@ dsa_status dsa_forward8(const dsa_shape* s, const dsa_inputs8* in, uint16_t* out
                         void* ws, size_t ws_bytes, void* stream) {
   dsa_status st = check_shape(s);
   if (st != DSA_OK) return st;
+  if (!attn8_rows_ok(s)) return DSA_ERR_UNSUPPORTED;
   if (in == nullptr || idx_out == nullptr) return DSA_ERR_INVALID_ARG;
   if (!indexer_ptrs_ok(in->q_I, in->q_scale, in->w, in->k_I, in->k_scale)) return DSA_ERR_INVALID_ARG;
   if (!attn8_ptrs_ok(in->q, in->kv8, in->kv_scale, out, ws)) return DSA_ERR_INVALID_ARG;
@@ -622,7 +628,9 @@ dsa_status dsa_forward8(const dsa_shape* s, const dsa_inputs8* in, uint16_t* out
     if ((st = run_select(c, s, L, ws, in->q_I, in->q_scale, in->w, in->k_I, in->k_scale, q0, cnt, idx_out)) != DSA_OK)
       return st;
   }
-  return run_attn8(c, s, in->q, in->kv8, in->kv_scale, idx_out, d_rows, out, lse, static_cast<char*>(ws) + front, need8);
+  // with every row dense the selection need not be read
+  return run_attn8(c, s, in->q, in->kv8, in->kv_scale, d_rows == s->T ? nullptr : idx_out, d_rows, out, lse,
+                   static_cast<char*>(ws) + front, need8);
 }
 
 dsa_status dsa_selftest_wait_timeout(void* stream) {

@@ -194,6 +194,27 @@ def test_unread_rows_may_hold_anything(T):
     c.check(*c.run(), rows=[0, T - 1])
 
 
+@pytest.mark.parametrize("B,T,S,H,d_k,page,lens", [
+    (1, 9, 140, 8, 576, 0, None),                      # eight queries' rows to a CTA, split keys
+    (2, 50, 333, 24, 576, 16, [51, 333]),              # queries that start inside a CTA's rows
+    (1, 300, 300, 72, 80, 0, None),                    # from the first position on
+    (3, 37, 200, 96, 80, 32, [37, 128, 200]),
+    (1, 200, 1000, 40, 576, 0, None),                  # one split a CTA
+])
+def test_dense_rows_of_several_queries(B, T, S, H, d_k, page, lens):
+    c = Case(B, T, S, H, d_k, 8, page, lens)
+    c.check(*c.run(dense=True), dense=True, rows=sorted({0, 1, 7, 8, T // 2, T - 2, T - 1}))
+
+
+def test_dense_agrees_with_every_key_selected():
+    """The same keys in the same chunks, in a CTA of one query and of several."""
+    c = Case(1, 160, 160, 40, 576, 160)
+    pos = torch.arange(160, device="cuda", dtype=torch.int32)
+    c.idx = torch.where(pos[None] <= pos[:, None], pos[None], torch.full_like(pos[None], -1))[None].contiguous()
+    (o1, l1), (o2, l2) = c.run(), c.run(dense=True)
+    assert torch.equal(o1, o2) and torch.equal(l1, l2)
+
+
 def test_dense_does_not_read_past_the_query():
     c = Case(1, 40, 100, 64, 576, 8)
     c.kv8[90:] = 0x7F

@@ -68,6 +68,10 @@ def test_rows_that_do_not_fit_an_int(L):
     s = ctypes.byref(shape(B=1 << 12, T=1 << 14, S=1 << 14))
     assert L.dsa_norm_rope(s, ctypes.byref(desc(Hq=128)), P, P, P, P, None) == UNSUPPORTED
     assert L.dsa_cache_write(ctypes.byref(shape(B=1 << 12, T=1 << 14, S=1 << 14, H_I=64)), *[P] * 9, None) == UNSUPPORTED
+    big = ctypes.byref(shape(B=1 << 12, T=1 << 12, S=1 << 12, H=128))
+    assert L.dsa_sparse_attn8(big, *[P] * 6, P, 1 << 40, None) == UNSUPPORTED
+    assert L.dsa_dense_attn8(big, *[P] * 5, P, 1 << 40, None) == UNSUPPORTED
+    assert L.dsa_workspace8_size(big) == 0
     assert L.dsa_cache_read(ctypes.byref(shape(B=1 << 12, T=1, S=1 << 20)), 0, 1 << 20, *[P] * 6, None) == UNSUPPORTED
 
 
