@@ -382,8 +382,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const bool packed = p.idx == nullptr;        // units are sequences
-  const int hs = blockIdx.x % p.hsplit;        // head rows [64 hs, 64 hs + 64) of the unit
-  const int rest = blockIdx.x / p.hsplit;
+  // head rows [64 hs, 64 hs + 64) of the unit; in a dense call the last
+  // queries, of the most keys, first
+  const int br = blockIdx.x % p.hsplit, rest = blockIdx.x / p.hsplit;
+  const int hs = packed ? p.hsplit - 1 - br : br;
   const int unit = rest / p.nsplit;            // b * T + t, or b
   const int split = rest - unit * p.nsplit;
   const int b = packed ? unit : unit / p.T;
