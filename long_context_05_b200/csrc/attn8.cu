@@ -105,6 +105,22 @@ struct Cfg {
   static_assert(2 * QT * kM <= 4 * PTERM, "staging");
 };
 
+// n / d for 0 <= n < 2^31 as a product with 2^32 (2^s / d - 1) rounded up, s
+// the first with 2^s >= d (Granlund and Montgomery): five divisions by every
+// warp of a CTA took 1200 cycles of its start.
+struct Divisor {
+  uint32_t mul, shift;
+  static Divisor of(int d) {
+    Divisor r{0, 0};
+    while ((1ull << r.shift) < (unsigned)d) ++r.shift;
+    r.mul = (uint32_t)(((1ull << 32) * ((1ull << r.shift) - (unsigned)d)) / (unsigned)d + 1);
+    return r;
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift);
+  }
+};
+
 struct Params {
   KvMap map;
   const uint16_t* q;
@@ -125,6 +141,7 @@ struct Params {
   // A unit is one query, with its H head rows, or in a dense call one
   // sequence, with all its T H; a CTA takes 64 head rows of one.
   int units, HR, nsplit, hsplit;
+  Divisor by_T, by_H, by_nsplit, by_hsplit;
   float scale_log2;      // tau log2(e)
   long long wait_ns;
   DevErr* err;
@@ -384,18 +401,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
   const bool packed = p.idx == nullptr;        // units are sequences
   // head rows [64 hs, 64 hs + 64) of the unit; in a dense call the last
   // queries, of the most keys, first
-  const int br = blockIdx.x % p.hsplit, rest = blockIdx.x / p.hsplit;
+  const int rest = p.by_hsplit(blockIdx.x), br = (int)blockIdx.x - rest * p.hsplit;
   const int hs = packed ? p.hsplit - 1 - br : br;
-  const int unit = rest / p.nsplit;            // b * T + t, or b
+  const int unit = p.by_nsplit(rest);          // b * T + t, or b
   const int split = rest - unit * p.nsplit;
-  const int b = packed ? unit : unit / p.T;
+  const int b = packed ? unit : p.by_T(unit);
   const int nrows = min(kM, p.HR - hs * kM);
-  const int t = packed ? (hs * kM + nrows - 1) / p.H : unit - b * p.T;   // the last query of the rows
+  const int t = packed ? p.by_H(hs * kM + nrows - 1) : unit - b * p.T;   // the last query of the rows
   const int Lb = p.map.len(b, threadIdx.x == 0 ? p.err : nullptr, ERR_SITE_ATTN8);
   const bool dense = packed || t < p.dense_rows;
   const int nslots = dense ? Lb - p.T + t + 1 : p.k;      // slots of these rows
   // an equal share of the row's chunks for every split
-  const int kc = ((nslots + kN - 1) / kN + p.nsplit - 1) / p.nsplit * kN;
+  const int kc = p.by_nsplit((nslots + kN - 1) / kN + p.nsplit - 1) * kN;
   const int slot0 = min(split * kc, nslots), slot1 = min(slot0 + kc, nslots);
   const int nchunks = (slot1 - slot0 + kN - 1) / kN;
 
@@ -415,19 +432,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
   if (warp >= kFirstSoftmax)
     load_q_rows(q4, p.q + ((size_t)unit * p.HR + hs * kM) * DK, nrows, warp - kFirstSoftmax, lane);
 
-  if (threadIdx.x == 0) {
-    mbar_init(q_ready, 8);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&kv_full[i], 32 * kGatherWarps);
-      mbar_init(&kv_empty[2 * i], 1);
-      mbar_init(&kv_empty[2 * i + 1], 1);
-      mbar_init(&par_full[i], 32);
-      mbar_init(&par_empty[i], 8);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 8);
-    }
-    mbar_init(mma_done, 1);
-    *abort_flag = 0;
+  if (warp == kParamWarp) {
+    // a lane's barrier (they lie side by side in this order) and its arrivals
+    const int i = lane;
+    const uint32_t arrivals = i == 0 ? 8                       // q_ready
+                              : i < 3 ? 32 * kGatherWarps      // kv_full
+                              : i < 7 ? 1                      // kv_empty
+                              : i < 9 ? 32                     // par_full
+                              : i < 11 ? 8                     // par_empty
+                              : i < 13 ? 1                     // s_full
+                              : i < 15 ? 8                     // p_full
+                                       : 1;                    // mma_done
+    if (i < C::NBARS) mbar_init(bars + i, arrivals);
+    if (i == 0) *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -660,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     const bool head_ok = r < nrows;
     // in a dense call the rows may be of several queries: this row's sees
     // slots up to `last`
-    const int last = packed ? Lb - p.T + h / p.H : 0x7fffffff;
+    const int last = packed ? Lb - p.T + p.by_H(h) : 0x7fffffff;
     float f_h = 0.f;
     split_q_rows<DK, DV>(q4, sw, lane, sQ, sP, sE);
     fence_proxy_async_smem();
@@ -1013,6 +1030,10 @@ cudaError_t launch_attn8(const LaunchCtx& c, const Attn8Args& a) {
   p.HR = pl.HR;
   p.hsplit = pl.hsplit;
   p.nsplit = pl.nsplit;
+  p.by_T = Divisor::of(p.T);
+  p.by_H = Divisor::of(p.H);
+  p.by_nsplit = Divisor::of(p.nsplit);
+  p.by_hsplit = Divisor::of(p.hsplit);
   p.scale_log2 = a.tau * 1.4426950408889634f;
   p.wait_ns = c.wait_ns;
   p.err = c.err;
