@@ -447,10 +447,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     if (i == 0) *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
-    tmem_alloc(tmem_slot, kTmemCols);
-    tmem_relinquish();
-  }
   if constexpr (DK % 128 != 0 && C::TAIL == 0) {
     // columns DK.. of the atoms of q (rows 0..127: both terms) and of the keys
     for (int i = threadIdx.x; i < 2 * (kM + kN) * 8; i += kThreads) {
@@ -460,10 +456,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     }
     fence_proxy_async_smem();
   }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  // TMEM is not needed before q is split: its allocation, 2000 cycles, runs
+  // beside the first gather, and barrier 1 tells the softmax warps
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+    tc_fence_before();
+    asm volatile("bar.arrive 1, 544;" ::: "memory");
+  }
+  auto tmem_base = [&]() -> uint32_t {
+    tc_fence_after();
+    return __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(tmem_slot), 0);
+  };
 
   const AbortSources ab{abort_flag, &p.err->code};
   const AbortSources no_abort{nullptr, nullptr};
@@ -493,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     auto help_q = [&]() {
       split_q_rows<DK, DV>(q4, warp - kFirstSoftmax, lane, sQ, sP, sE);
       fence_proxy_async_smem();
-      asm volatile("bar.arrive 1, 512;" ::: "memory");
+      asm volatile("bar.arrive 1, 544;" ::: "memory");
     };
     for (int j = 0; j < nchunks; ++j) {
       const int rg = j & 1;
@@ -590,6 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
       const bool leader = elect_one() != 0;
       bool ok = wwait(q_ready, 0);
       if (!ok) fail(4);
+      const uint32_t tmem = tmem_base();                 // (q is in it)
       int qk = 0, pv = 0;
       // S = q K^T of chunk qk: both terms of q over the key columns, in steps of 32
       auto issue_qk = [&]() {
@@ -681,7 +687,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     float f_h = 0.f;
     split_q_rows<DK, DV>(q4, sw, lane, sQ, sP, sE);
     fence_proxy_async_smem();
-    bar_sync(1, 512);                                    // with the gather warps' rows
+    bar_sync(1, 544);                                    // with the gather warps' rows and the TMEM
+    const uint32_t tmem = tmem_base();
     if (nchunks > 0) {
       f_h = sE[r];
       if constexpr (C::QT > 0) {
@@ -886,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(tmem_base(), kTmemCols);
   }
 }
 
