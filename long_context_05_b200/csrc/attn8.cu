@@ -142,6 +142,7 @@ struct Params {
   // sequence, with all its T H; a CTA takes 64 head rows of one.
   int units, HR, nsplit, hsplit;
   Divisor by_T, by_H, by_nsplit, by_hsplit;
+  int ahead;             // CTAs of a wave: the next on this SM is about so many on
   float scale_log2;      // tau log2(e)
   long long wait_ns;
   DevErr* err;
@@ -241,6 +242,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+
+__device__ __forceinline__ void prefetch_l2(const void* a) { asm volatile("prefetch.global.L2 [%0];" ::"l"(a)); }
 
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -548,6 +551,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
       if (PAGED && v >= 0 && r < 0) report_error(p.err, DSA_ERR_DEVICE_BOUNDS, ERR_SITE_ATTN8 | (1u << 8));
       return r;
     };
+    // the rows of q, and of indices, that the next CTA on this SM begins with,
+    // on their way to L2
+    const int x = (int)blockIdx.x + p.ahead;
+    if (x < (int)gridDim.x) {
+      const int rest2 = p.by_hsplit(x), br2 = x - rest2 * p.hsplit, unit2 = p.by_nsplit(rest2);
+      const int hs2 = packed ? p.hsplit - 1 - br2 : br2;
+      const char* q2 = reinterpret_cast<const char*>(p.q + ((size_t)unit2 * p.HR + hs2 * kM) * DK);
+      for (int i = lane * 128; i < min(kM, p.HR - hs2 * kM) * DK * 2; i += 32 * 128) prefetch_l2(q2 + i);
+      if (!packed)
+        for (int i = lane * 32; i < p.k; i += 32 * 32) prefetch_l2(p.idx + (size_t)unit2 * p.k + i);
+    }
     int ip[4];
     float s_cur[4];
 #pragma unroll
@@ -1042,6 +1056,7 @@ cudaError_t launch_attn8(const LaunchCtx& c, const Attn8Args& a) {
   p.by_nsplit = Divisor::of(p.nsplit);
   p.by_hsplit = Divisor::of(p.hsplit);
   p.scale_log2 = a.tau * 1.4426950408889634f;
+  p.ahead = c.num_sms;
   p.wait_ns = c.wait_ns;
   p.err = c.err;
   if (p.nsplit > 1) {
