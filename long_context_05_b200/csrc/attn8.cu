@@ -288,56 +288,56 @@ __device__ __forceinline__ void tmem_scale(uint32_t addr, float alpha) {
   tmem_wait_st();
 }
 
-// Four head rows of q (rows 4 w .. 4 w + 3 of the CTA's 64) in two e4m3 terms,
+// R head rows of q (rows r0 .. r0 + R - 1 of the CTA's 64) in two e4m3 terms,
 // by one warp.  A step is 32 vectors of eight columns: the full steps of each
 // row, then what is left of the rows' columns, 32 / RV rows to a step, so that
 // a lane's place in shared memory is known once for all rows but for the
 // swizzle.  A row's exponent comes from its maximum over the warp.
-template <int DK>
+template <int DK, int R>
 struct QRows {
   static constexpr int FULL = DK / 256;                  // full steps of a row
+  static constexpr int DIV = FULL > 0 ? FULL : 1;
   static constexpr int RV = (DK - FULL * 256) / 8 <= 8 ? 8 : 16;   // lanes of a row in the last steps
-  static constexpr int TAILS = 4 * RV / 32;              // last steps
-  static constexpr int STEPS = 4 * FULL + TAILS;
+  static constexpr int TAILS = (R * RV + 31) / 32;       // last steps
+  static constexpr int STEPS = R * FULL + TAILS;
   uint4 v[STEPS];
-};
-template <int DK>
-__device__ __forceinline__ void load_q_rows(QRows<DK>& q4, const uint16_t* q, int heads, int w, int lane) {
-  using Q = QRows<DK>;
-  const uint16_t* q0 = q + (size_t)4 * w * DK;
+  __device__ __forceinline__ void load(const uint16_t* q, int heads, int r0, int lane) {
+    const uint16_t* q0 = q + (size_t)r0 * DK;
 #pragma unroll
-  for (int s = 0; s < Q::STEPS; ++s) {
-    const bool full = s < 4 * Q::FULL;
-    const int row = full ? s / (Q::FULL > 0 ? Q::FULL : 1) : (s - 4 * Q::FULL) * (32 / Q::RV) + lane / Q::RV;
-    const int col = full ? (s % (Q::FULL > 0 ? Q::FULL : 1)) * 256 + lane * 8 : Q::FULL * 256 + (lane % Q::RV) * 8;
-    q4.v[s] = make_uint4(0u, 0u, 0u, 0u);
-    if (4 * w + row < heads && col < DK) q4.v[s] = __ldg(reinterpret_cast<const uint4*>(q0 + row * DK + col));
+    for (int s = 0; s < STEPS; ++s) {
+      const bool full = s < R * FULL;
+      const int row = full ? s / DIV : (s - R * FULL) * (32 / RV) + lane / RV;
+      const int col = full ? s % DIV * 256 + lane * 8 : FULL * 256 + (lane % RV) * 8;
+      v[s] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < R && r0 + row < heads && col < DK) v[s] = __ldg(reinterpret_cast<const uint4*>(q0 + row * DK + col));
+    }
   }
-}
-template <int DK, int DV>
-__device__ __forceinline__ void split_q_rows(const QRows<DK>& q4, int w, int lane, uint8_t* sQ, uint8_t* sP, float* sE) {
+};
+template <int DK, int DV, int R>
+__device__ __forceinline__ void split_q_rows(const QRows<DK, R>& q4, int r0, int lane, uint8_t* sQ, uint8_t* sP,
+                                             float* sE) {
   using C = Cfg<DK, DV>;
-  using Q = QRows<DK>;
-  uint32_t m[4] = {0u, 0u, 0u, 0u};
+  using Q = QRows<DK, R>;
+  uint32_t m[R] = {};
 #pragma unroll
   for (int s = 0; s < Q::STEPS; ++s) {
     const uint32_t x = max_abs8(q4.v[s]);
-    if (s < 4 * Q::FULL) {
-      m[s / (Q::FULL > 0 ? Q::FULL : 1)] = max(m[s / (Q::FULL > 0 ? Q::FULL : 1)], x);
+    if (s < R * Q::FULL) {
+      m[s / Q::DIV] = max(m[s / Q::DIV], x);
     } else {
 #pragma unroll
       for (int i = 0; i < 32 / Q::RV; ++i) {
-        const int row = (s - 4 * Q::FULL) * (32 / Q::RV) + i;
-        m[row] = max(m[row], lane / Q::RV == i ? x : 0u);
+        const int row = (s - R * Q::FULL) * (32 / Q::RV) + i;
+        if (row < R) m[row] = max(m[row], lane / Q::RV == i ? x : 0u);
       }
     }
   }
-  float inv[4];
+  float inv[R];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < R; ++i) {
     const int e = pow2_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, m[i]) << 16));
     inv[i] = __uint_as_float((uint32_t)(127 - e) << 23);
-    if (lane == i) sE[4 * w + i] = __uint_as_float((uint32_t)(127 + e) << 23);
+    if (lane == i) sE[r0 + i] = __uint_as_float((uint32_t)(127 + e) << 23);
   }
   // both terms of eight columns: 8 bytes at d and at d + to_lo
   auto put = [&](const uint4& v, float f, uint8_t* d, int to_lo) {
@@ -350,17 +350,19 @@ __device__ __forceinline__ void split_q_rows(const QRows<DK>& q4, int w, int lan
   };
 #pragma unroll
   for (int s = 0; s < Q::STEPS; ++s) {
-    if (s < 4 * Q::FULL) {
-      const int i = s / (Q::FULL > 0 ? Q::FULL : 1), u = s % (Q::FULL > 0 ? Q::FULL : 1), rr = 4 * w + i;
+    if (s < R * Q::FULL) {
+      const int i = s / Q::DIV, u = s % Q::DIV, rr = r0 + i;
       const int c16 = (lane & 15) >> 1, in_atom = (lane >> 4) * (kM * 128);
       const int at = rr * 128 + ((c16 ^ (rr & 7)) << 4) + (lane & 1) * 8 + in_atom;
       // q's TMEM columns are staged in the P buffers: [term][atom][64 rows x 128 bytes]
       if (u * 256 < C::QT) put(q4.v[s], inv[i], sP + (u * 2) * (kM * 128) + at, (C::QT / 128) * (kM * 128));
       else put(q4.v[s], inv[i], sQ + (u * 2 - C::QT / 128) * (kM * 128) + at, C::QPIECE);
     } else {
-      const int i = (s - 4 * Q::FULL) * (32 / Q::RV) + lane / Q::RV, rr = 4 * w + i, l = lane % Q::RV;
-      if (Q::FULL * 256 + l * 8 >= DK) continue;
-      const float f = i == 0 ? inv[0] : i == 1 ? inv[1] : i == 2 ? inv[2] : inv[3];
+      const int i = (s - R * Q::FULL) * (32 / Q::RV) + lane / Q::RV, rr = r0 + i, l = lane % Q::RV;
+      if (i >= R || Q::FULL * 256 + l * 8 >= DK) continue;
+      float f = inv[0];
+#pragma unroll
+      for (int y = 1; y < R; ++y) f = i == y ? inv[y] : f;
       uint8_t* d = C::TAIL != 0 ? sQ + C::QSF * (kM * 128) + rr * 64 + (((l >> 1) ^ ((rr >> 1) & 3)) << 4)
                                 : sQ + rr * 128 + (((l >> 1) ^ (rr & 7)) << 4);
       put(q4.v[s], f, d + (l & 1) * 8, C::QPIECE);
@@ -422,18 +424,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
   const int32_t* irow = dense ? nullptr : p.idx + (size_t)unit * p.k;
   // index of slot s of this split; -1 past the end and for an empty slot
   auto load_idx = [&](int s) -> int { return s < slot1 ? (dense ? s : irow[s]) : -1; };
-  // q's rows are on their way while the barriers and TMEM are set up: the
-  // softmax warps take rows 0..31, the gather warps 32..63, behind the indices
-  // of their first two chunks
+  // q's rows are on their way while the barriers are set up: six to a softmax
+  // warp, from the first, and two to a gather warp, behind its first chunk
+  // (four to each: the softmax warps waited 2500 cycles for the others)
   const int kl = 16 * (warp - kFirstGather) + (lane & 15);
   int i_cur = -1, i_next = -1;
   if (warp >= kFirstGather) {
     i_cur = load_idx(slot0 + kl);
     i_next = load_idx(slot0 + kN + kl);
   }
-  QRows<DK> q4;
-  if (warp >= kFirstSoftmax)
-    load_q_rows(q4, p.q + ((size_t)unit * p.HR + hs * kM) * DK, nrows, warp - kFirstSoftmax, lane);
+  const uint16_t* q0 = p.q + ((size_t)unit * p.HR + hs * kM) * DK;
+  QRows<DK, 4> q4;
+  QRows<DK, 2> q2;                             // rows 32..47, 48..63
+  if (warp >= kFirstSoftmax) {
+    if (warp < kFirstGather) q4.load(q0, nrows, 4 * (warp - kFirstSoftmax), lane);
+    q2.load(q0, nrows, 32 + 2 * (warp - kFirstSoftmax), lane);
+  }
 
   if (warp == kParamWarp) {
     // a lane's barrier (they lie side by side in this order) and its arrivals
@@ -499,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     int r_cur = row_of(i_cur);
     // this warp's rows of q, behind the first chunk
     auto help_q = [&]() {
-      split_q_rows<DK, DV>(q4, warp - kFirstSoftmax, lane, sQ, sP, sE);
+      split_q_rows<DK, DV>(q2, 48 + 2 * g, lane, sQ, sP, sE);
       fence_proxy_async_smem();
       asm volatile("bar.arrive 1, 544;" ::: "memory");
     };
@@ -699,7 +705,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     // slots up to `last`
     const int last = packed ? Lb - p.T + p.by_H(h) : 0x7fffffff;
     float f_h = 0.f;
-    split_q_rows<DK, DV>(q4, sw, lane, sQ, sP, sE);
+    split_q_rows<DK, DV>(q4, 4 * sw, lane, sQ, sP, sE);
+    split_q_rows<DK, DV>(q2, 32 + 2 * sw, lane, sQ, sP, sE);
     fence_proxy_async_smem();
     bar_sync(1, 544);                                    // with the gather warps' rows and the TMEM
     const uint32_t tmem = tmem_base();
