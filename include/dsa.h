@@ -411,8 +411,9 @@ DSA_API size_t dsa_norm_rope_workspace_size(const dsa_shape* shape, const dsa_no
 /* Gradients of dsa_norm_rope: from its inputs q, k (not needed and may be
  * NULL when norm_cols is 0) and the gradients dq_out, dk_out of its outputs,
  * dq, dk BF16 (dq_out's and dk_out's own buffers are allowed) and the norm
- * weights' dq_weight, dk_weight FP32 [norm_cols] (written, not added to;
- * NULL: not wanted).  The weight sums run in a fixed order.
+ * weights' dq_weight, dk_weight FP32 [norm_cols] (written, not added to, zeros
+ * for a side without heads; NULL: not wanted).  The weight sums run in a fixed
+ * order.
  * ws: dsa_norm_rope_workspace_size bytes (may be NULL when no weight gradient
  * is wanted). */
 DSA_API dsa_status dsa_norm_rope_backward(const dsa_shape* shape, const dsa_norm_rope_desc* desc, const uint16_t* q,
@@ -428,8 +429,9 @@ DSA_API dsa_status dsa_norm_rope_backward(const dsa_shape* shape, const dsa_norm
  * Each of the three parts may be left out (its three pointers NULL).
  * A row's scale is 2^e with the smallest e >= -48 for which
  * max|x| <= 448 * 2^e, its bytes are e4m3(x * 2^-e) rounded to nearest even
- * (values past 240 * 2^120 are stored as that; x holds no NaN).  Other rows of the caches are left as they are; a row whose
- * page is unmapped is reported and dropped. */
+ * (values past 240 * 2^120 are stored as that; x holds no NaN).  Other rows of
+ * the caches are left as they are; a row whose page is unmapped is reported and
+ * dropped. */
 DSA_API dsa_status dsa_cache_write(const dsa_shape* shape, const uint16_t* kv, uint8_t* kv8, float* kv_scale,
                            const uint16_t* k_I, uint8_t* kI8, float* kI_scale, const uint16_t* q_I, uint8_t* qI8,
                            float* qI_scale, void* stream);

@@ -662,7 +662,7 @@ extern "C" dsa_status dsa_norm_rope_backward(const dsa_shape* s, const dsa_norm_
     if (ws == nullptr || ws_bytes < dsa_norm_rope_workspace_size(s, d) || (reinterpret_cast<uintptr_t>(ws) & 3u))
       return DSA_ERR_WORKSPACE;
     float* part = static_cast<float*>(ws);
-    float* dw[2] = {d->Hq > 0 ? dq_weight : nullptr, d->Hk > 0 ? dk_weight : nullptr};
+    float* dw[2] = {dq_weight, dk_weight};         // a side without heads: the sum over no rows
     for (int i = 0; i < 2; ++i) {
       if (dw[i] == nullptr) continue;
       p.side[i].dw_part = part;

@@ -382,6 +382,26 @@ def _step(wl, raw, cache, s0, s1, page, table, nw, freq, fused_ws=False):
     return sh, part, (qI8, qs), out, lse, idx
 
 
+def test_calls_at_once_on_two_streams():
+    """Split and unsplit, selected and dense calls side by side, each with a workspace of its own."""
+    cases = [(Case(2, 1, 1500, 128, 576, 700, 16, [900, 1500], True).select(), False),
+             (Case(1, 90, 400, 64, 576, 128).select(), False),
+             (Case(1, 70, 300, 24, 576, 8, seed=1), True), (Case(2, 1, 2000, 16, 576, 8, 0, None, True), True)]
+    want = [c.run(dense=d) for c, d in cases]
+    ws = [dsa.alloc_workspace8(c.shape) for c, _ in cases]
+    streams = [torch.cuda.Stream() for _ in cases[:2]]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(12):
+        c, d = cases[i % 4]
+        with torch.cuda.stream(streams[i % 4 // 2]):
+            got.append((i % 4, c.run(dense=d, ws=ws[i % 4])))
+    torch.cuda.synchronize()
+    assert dsa.device_error()[0] == 0
+    for i, (o, l) in got:
+        assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1]), i
+
+
 @pytest.mark.parametrize("page", [0, 32])
 def test_prefill_then_decode_through_every_operator(page):
     """A prefill of 70 tokens, then three decode steps, each from raw rows;

@@ -207,6 +207,15 @@ def test_same_bits_again_on_another_stream_and_from_a_graph():
         assert all(torch.equal(a[n], b[n]) for n in a)
 
 
+def test_weight_gradient_of_a_side_without_heads_is_zero():
+    c = Case(1, 5, 9, 2, 0, 64, 64, 32)
+    dx, dw = torch.empty_like(c.x["q"]), {n: torch.full((64,), 77.0, device="cuda") for n in "qk"}
+    dsa.norm_rope_backward(c.shape, c.desc, c.x["q"], None, c.dy["q"], None, dx, None, dw["q"], dw["k"],
+                           dsa.alloc_norm_rope_workspace(c.shape, c.desc))
+    assert torch.equal(dw["q"], c.backward()[1]["q"])
+    assert bool((dw["k"] == 0).all()) and dsa.device_error()[0] == 0
+
+
 def test_lengths_out_of_range_are_reported():
     c = Case(2, 3, 50, 2, 1, 80, 64, 16, lens=[50, 51])
     c.forward()
