@@ -169,13 +169,19 @@ void note_launches(int n);
 
 // Dynamic shared memory past what a kernel is allowed by itself: asked for
 // once per kernel and device (`granted`: the kernel's own array, bytes granted
-// so far), since asking costs a launch a fifth of its time.
+// so far), since asking costs a launch a fifth of its time.  `whole`: the
+// kernel runs with all of an SM's memory as shared memory, not what one wave
+// of it needs.
 constexpr int kMaxDevices = 64;
 template <class Kernel>
-cudaError_t grant_smem(Kernel kernel, int bytes, int device, std::atomic<int>* granted) {
+cudaError_t grant_smem(Kernel kernel, int bytes, int device, std::atomic<int>* granted, bool whole = false) {
   if (bytes <= granted[device].load(std::memory_order_acquire)) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
+  if (whole) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+  }
   int seen = granted[device].load(std::memory_order_relaxed);
   while (seen < bytes && !granted[device].compare_exchange_weak(seen, bytes, std::memory_order_release)) {
   }

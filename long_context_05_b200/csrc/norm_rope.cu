@@ -13,7 +13,7 @@
 // so the bound is HBM: 4 bytes per element forward, 6 backward.  All rows of
 // a side lie one behind the other, so a tile of them is one contiguous piece
 // of memory whatever its heads and tokens.  Every warp works by itself: it
-// takes a run of tiles of about 4.5 KB and keeps kStages of them on their way
+// takes a run of tiles of about 4.5 KB and keeps two of them on their way
 // into shared memory of its own by bulk copies, so no registers hold loads in
 // flight and no warp waits for another.  A row is worked on by G lanes (16 at
 // 576 columns, 8 at 128; U rows of each group at a time where rows are short,
@@ -27,11 +27,11 @@
 // meets the same columns in every row), are added in a fixed order over the
 // block and then over the blocks: the same call gives the same bits.
 //
-// Measured: 8192 tokens of 129 rows of 576 columns forward 458 us, 5.3 TB/s
-// (2.43 GB; issue slots 47 % busy, DRAM 67 % by its own count); 2062 such
-// tokens forward and backward 288 us, 5.3 TB/s; 4096 tokens of 65 rows of 128
-// columns forward and backward 89 us, 3.8 TB/s: there a row is only 256 bytes,
-// and its reductions, square root and addresses keep the issue slots busy.
+// Measured: 8192 tokens of 129 rows of 576 columns forward 425 us with a cold
+// L2, 5.7 TB/s (2.43 GB; 388 us, 6.3 TB/s back to back); 2062 such tokens
+// forward and backward 285 us, 5.4 TB/s (265, 5.8); 4096 tokens of 65 rows of
+// 128 columns forward and backward 89 us, 3.8 TB/s: short kernels of a dozen
+// tiles a warp, where the start and the end weigh.
 #include "internal.h"
 #include "sm100.cuh"
 
@@ -176,8 +176,13 @@ __device__ __forceinline__ void rotate8(F8& z, const F8& o, const float2* cs, in
   }
 }
 
-// Blocks of an SM that the registers leave room for.
-constexpr int blocks_per_sm(int V, bool back) { return V >= 4 ? (back ? 3 : 5) : (back ? 4 : 5); }
+// Blocks of an SM that the registers leave room for.  Long rows want registers
+// (140 and 146 at 576 columns; forward 4096 tokens of 129 rows took 235 us
+// with five blocks of 96, 229 with four of 128, 196 with three, 261 with two;
+// backward 307 with three, 331 and 445 with four and two), short rows warps
+// (4096 tokens of 65 rows of 128: 32.9 us with five, 35.5 and 38 with four and
+// three; forward and backward 89 with five and four, 96 with five and five).
+constexpr int blocks_per_sm(int V, bool back) { return V >= 4 ? 3 : back ? 4 : 5; }
 
 template <int G, int V, int MODE, bool BACK>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(V, BACK)) norm_rope_kernel(NrParams p) {
@@ -209,11 +214,15 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(V, BACK)) norm_rope_ke
     bulk_load(d, (BACK ? s.dy : s.x) + at, bytes, &full[st]);
     if (BACK && need_x) bulk_load(d + p.tensor_bytes, s.x + at, bytes, &full[st]);
   };
-  pdl_launch_dependents();
   if (lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
     fence_mbar_init();
   }
+  // What follows on the stream may start: at once where rows are short (a
+  // training pass of 4096 tokens of 65 rows of 128: 89.6 us, 91.3 at the end),
+  // behind the tiles where they are long (2062 tokens of 129 rows of 576: 265
+  // us, 269 at the start).
+  if (V < 4) pdl_launch_dependents();
   pdl_wait();                                     // nothing of global memory is read before this
   if (lane == 0) {
     for (int i = tile0; i < tile1 && i < tile0 + kStages; ++i) load_tile(i);
@@ -432,6 +441,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(V, BACK)) norm_rope_ke
     n0 += q;
     off += p.rt - q * s.H;
   }
+  if (V >= 4) pdl_launch_dependents();
   if constexpr (BACK) {
     if (s.dw_part == nullptr) return;
     // the groups' sums, in group order: first over the groups of a warp by
@@ -547,7 +557,12 @@ template <int G, int V, int MODE, bool BACK>
 cudaError_t launch_mode(const LaunchCtx& c, const NrParams& p, size_t smem) {
   auto kern = norm_rope_kernel<G, V, MODE, BACK>;
   static std::atomic<int> granted[kMaxDevices];
-  const cudaError_t e = grant_smem(kern, (int)smem, c.device, granted);
+  // Kernels of three blocks an SM ask for all of its shared memory: one that
+  // starts beside the end of the other, where that one has divided the memory
+  // for its own needs, had room for two (a forward and a backward pass in turn
+  // took 330 us, 101 and 160 alone).  Those of short rows fill it anyway, and
+  // took 92 us instead of 90 with it.
+  const cudaError_t e = grant_smem(kern, (int)smem, c.device, granted, V >= 4);
   if (e != cudaSuccess) return e;
   const cudaError_t l = launch_pdl(kern, dim3((unsigned)(p.side[0].blocks + p.side[1].blocks)), dim3(kThreads), smem,
                                    c.stream, p);
