@@ -58,8 +58,10 @@
 // count double on the tensor cores); kept up for seconds, 1280 us at the
 // board's power limit.  Two chunks take 7400 cycles of a CTA: the MMAs 6475,
 // and 925 of waiting for the second chunk's softmax, which is longer than the
-// P V it runs under.  To its first logits a CTA takes about 10000 cycles (q's
-// split 3400 of them, the first gather beside it), for its output 3500.  Sixteen
+// P V it runs under.  To its first logits a CTA takes about 10000 cycles, 5500 of
+// them until q and the first chunk are there (150 KB at 27 bytes a clock from
+// L2 with every SM asking; a third fewer instructions in q's split changed
+// nothing), for its output 3500 (the stores' way out).  Sixteen
 // softmax warps were slower (1575 us: the MMA warp lost issue slots), and so
 // were CTAs that stay and place the next tile's q under the end of the last
 // (1150 us for 1160 then, but dense calls 515 for 444: the hardware's own
