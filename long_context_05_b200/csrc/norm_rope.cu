@@ -181,11 +181,13 @@ __device__ __forceinline__ void rotate8(F8& z, const F8& o, const float2* cs, in
 // with five blocks of 96, 229 with four of 128, 196 with three, 261 with two;
 // backward 307 with three, 331 and 445 with four and two), short rows warps
 // (4096 tokens of 65 rows of 128: 32.9 us with five, 35.5 and 38 with four and
-// three; forward and backward 89 with five and four, 96 with five and five).
-constexpr int blocks_per_sm(int V, bool back) { return V >= 4 ? 3 : back ? 4 : 5; }
+// three; forward and backward 89 with five and four, 96 with five and five;
+// forward with pairs (i, i + r/2), which do not fit 96 registers, 40.0 with
+// five, 38.6 with four).
+constexpr int blocks_per_sm(int V, bool back, bool half) { return V >= 4 ? 3 : back || half ? 4 : 5; }
 
 template <int G, int V, int MODE, bool BACK>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm(V, BACK)) norm_rope_kernel(NrParams p) {
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(V, BACK, MODE == kHalf)) norm_rope_kernel(NrParams p) {
   extern __shared__ uint4 smem4[];
   __shared__ uint64_t full_bar[kWarps][kStages];
   constexpr int GP = 32 / G;                      // groups of a warp
@@ -532,7 +534,7 @@ size_t smem_of(const dsa_norm_rope_desc* d, bool back) {
 // Blocks resident at once: what shared memory and registers allow.
 int resident_blocks(const dsa_norm_rope_desc* d, bool back, int num_sms) {
   int n = (int)(227 * 1024 / (smem_of(d, back) + 1280));
-  const int regs = blocks_per_sm(d->D > 256 ? 4 : 1, back);
+  const int regs = blocks_per_sm(d->D > 256 ? 4 : 1, back, d->rope_cols > 0 && d->interleaved == 0);
   if (n > regs) n = regs;
   return (n < 1 ? 1 : n) * num_sms;
 }
