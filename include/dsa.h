@@ -454,8 +454,11 @@ DSA_API size_t dsa_workspace8_size(const dsa_shape* shape);
  * bytes and kv_scale [B, S] FP32 (paged: pools of rows); any finite scales in
  * [2^-100, 2^100].  Selected rows hold no NaN bytes; other rows may hold
  * anything.  The products are those of the given bytes with q split into two
- * e4m3 terms and of the probabilities split likewise, accumulated in FP32;
- * out is rounded to BF16 once.  The two modes give the same results; calls of
+ * e4m3 terms (off by 2^-17.8 of the head row's largest at most) and with the
+ * probabilities split into an e4m3 and an e5m2 term (2^-8 of themselves, as
+ * BF16 ones, and together at most 2^-9 of the largest product of a
+ * probability and its row's scale, of more than 2048 keys of each 128 keys'
+ * largest), accumulated in FP32; out is rounded to BF16 once.  The two modes give the same results; calls of
  * few rows split their keys over the SMs and need the workspace.  B T H is
  * below 2^31. */
 DSA_API dsa_status dsa_sparse_attn8(const dsa_shape* shape, const uint16_t* q, const uint8_t* kv8,

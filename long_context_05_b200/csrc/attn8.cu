@@ -5,23 +5,32 @@
 // a = tau log2(e):
 //   x_k = a s_k (q . k8_k) + log2 s_k,        R a running reference,
 //   P_k = 2^(x_k - R) = 2^(logit_k - R) s_k,  l = sum_k P_k / s_k,
-//   out = sum_k P_k k8_k[:d_v] / l,           lse = (R + log2 l) ln 2.
+//   out = sum_k P_k k8_k[:d_v] / l,           lse = (R + log2 l) ln 2
+// (s_k outside a in units of a power of two near the first key's).
 // The token's scale is folded into the exponent, so the cached bytes go to
 // the tensor cores as they are, in both products: no dequantised copy of a
 // key exists anywhere, a key costs 576 bytes of shared memory instead of
 // 1152, and the gather moves half the bytes of the BF16 cache.
 //
-// kind::f8f6f4 multiplies e4m3 by e4m3 at twice the BF16 rate, so the other
-// operand is split in two e4m3 terms and every product runs twice, at the
+// kind::f8f6f4 multiplies 8-bit floats at twice the BF16 rate, so the other
+// operand is split in two 8-bit terms and every product runs twice, at the
 // cost of one BF16 product:
-//   * q = 2^e (q_hi + q_lo), 2^e per head row with max|q| <= 448 * 2^e.  A
-//     BF16 number has 8 significant bits and e4m3 four, so the two terms give
-//     q exactly down to 2^-10 of the row's largest, and within 2^-19 of it
-//     below (e4m3's subnormal step);
-//   * P = P_hi + P_lo, rounded to nearest at 2^-8 of P at worst and 2^-10.6
-//     in the mean square (one BF16 number: 2^-9 and 2^-9.3).  R is kept so
-//     that the largest P of a row is at least 2^4: e4m3's subnormal half step
-//     is then 2^-14 of it or less.
+//   * q = 2^e (q_hi + q_lo), both e4m3, 2^e per head row with max|q| <= 448 *
+//     2^e.  A BF16 number has 8 significant bits and e4m3 four, so the two
+//     terms give q exactly down to 2^-10 of the row's largest, and within
+//     2^-17.8 of it below (half of e4m3's subnormal step over 224);
+//   * P = P_hi (e4m3) + P_lo (e5m2): off by 2^-8 of P at worst, as one BF16
+//     number, and 2^-9.6 in the mean square, down to P = 2^-6, and by 2^-14
+//     or less below.  (With P_lo in e4m3, as precise again above, what lies
+//     below 2^-10 was lost: a tail of 8191 keys ten nats under one key a
+//     quarter of the output.)
+// So that 2^-14 stays small beside what a row holds, however long it is, R
+// keeps the largest P of a row between 2^kHead and 2^kTop: 2048 keys lose at
+// most 2048 * 2^-14 / 2^kHead = 2^-9 of the largest one.  Where a part has
+// more keys, R also comes down when the largest P of a chunk falls below
+// 2^(kHead - kDrop): a chunk then loses at most 128 * 2^-14 / 2^(kHead -
+// kDrop) = 2^-9 of its own largest.  The accumulator, FP32, has the range for
+// that; kDepth bounds how far R lies under the highest it ever was.
 // Logits, P before its rounding, l and the output accumulate in FP32.
 //
 // Work split.  A CTA takes 64 head rows and all value columns: heads of one
@@ -50,8 +59,7 @@
 // constants; warps 2-9 are the softmax, warps 10-17 gather 16 keys each with
 // 16-byte cp.async that arrive on the region's barrier by themselves.  Four
 // softmax threads share a head row (32 keys each) and exchange their maxima
-// through shared memory.  R moves only when a chunk's maximum exceeds it by
-// kSlack, and then the accumulator is rescaled once.
+// through shared memory.  When R moves, the accumulator is rescaled once.
 //
 // Measured (576 / 512).  2048 queries of 128 heads over 2048 selected keys
 // each: 1106 us, 1056 TFLOP/s of the 1168 GFLOP counted once (the two terms
@@ -83,8 +91,14 @@ constexpr int kM = 64;                 // heads per CTA
 constexpr int kMmaWarp = 0, kParamWarp = 1, kFirstSoftmax = 2, kFirstGather = 10, kGatherWarps = 8;
 constexpr int kThreads = 32 * (kFirstGather + kGatherWarps);
 constexpr uint32_t kTmemCols = 512;
-constexpr float kHead = 4.f;           // log2 of the largest P of a row when R is set
-constexpr float kSlack = 4.75f;        // how far a maximum may pass before R moves (2^(4 + 4.75) < 448)
+constexpr float kHead = 6.f;           // log2 of the largest P of a row when R is set (P is then exact)
+constexpr float kTop = 8.75f;          // ... and at most (2^8.75 < 448)
+// (With kHead 4, 5, 6 and 8, on keys of spread norms, R moves in 9.1, 9.7, 10.4
+// and 12.3 of 15 chunks of a warp: 1311, 1314 and 1320 us with 4, 5 and 6 on
+// 2048 queries of 128 heads over 2048 keys.)
+constexpr float kDrop = 4.f;           // how far a chunk's maximum may fall short of kHead
+constexpr int kLongPart = 2048;        // in parts of more keys than this
+constexpr float kDepth = 24.f;         // how far R may come down from the highest it was
 
 template <int DK, int DV>
 struct Cfg {
@@ -111,7 +125,7 @@ struct Cfg {
   static constexpr int OFF_E = OFF_MX + 2 * 4 * kM * 4;  // [64] 2^e of the head rows
   static constexpr int OFF_BAR = OFF_E + kM * 4;
   static constexpr int NBARS = 1 + 2 + 4 + 2 + 2 + 2 + 2 + 1;
-  static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;
+  static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;   // TMEM's base, abort flag, scale unit
   static constexpr int BYTES = OFF_MISC + 16;
   static_assert(BYTES <= 232448, "shared memory per CTA");
   static_assert(OFF_KV % 1024 == 0 && OFF_P % 1024 == 0 && OFF_BAR % 8 == 0, "alignment");
@@ -168,20 +182,22 @@ __device__ __forceinline__ int pow2_exponent(float amax) {
   const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
   return min(max(e, -100), 120);
 }
-__device__ __forceinline__ uint32_t e4m3x2_of_half2(__half2 h) {
-  return (uint32_t)__nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<__half2_raw*>(&h), __NV_SATFINITE, __NV_E4M3);
+template <__nv_fp8_interpretation_t TO>
+__device__ __forceinline__ uint32_t fp8x2_of_half2(__half2 h) {
+  return (uint32_t)__nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<__half2_raw*>(&h), __NV_SATFINITE, TO);
 }
 __device__ __forceinline__ __half2 half2_of_e4m3x2(uint32_t v) {
   return __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)v, __NV_E4M3));
 }
-// two e4m3 terms of a pair of numbers (|a|, |b| <= 448): low 16 bits of hi, lo
+// two terms of a pair of numbers (|a|, |b| <= 448), e4m3 and LO: low 16 bits of hi, lo
+template <__nv_fp8_interpretation_t LO>
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
   const __half2 h = __floats2half2_rn(a, b);
-  hi = e4m3x2_of_half2(h);
-  lo = e4m3x2_of_half2(__hsub2(h, half2_of_e4m3x2(hi)));
+  hi = fp8x2_of_half2<__NV_E4M3>(h);
+  lo = fp8x2_of_half2<LO>(__hsub2(h, half2_of_e4m3x2(hi)));
 }
 
-// D[tmem] (+)= A B^T, e4m3, the M = 64 form that uses all lanes; A in shared
+// D[tmem] (+)= A B^T, 8-bit floats, the M = 64 form that uses all lanes; A in shared
 // memory or in TMEM (in lanes 0-63 and again in 64-127).  The two terms of A
 // meet the same B one after the other: the first MMA leaves B in the
 // collector and the second takes it from there, which halves the reads of
@@ -359,7 +375,8 @@ __device__ __forceinline__ void split_q_rows(const QRows<DK, R>& q4, int r0, int
     const uint32_t x[4] = {v.x, v.y, v.z, v.w};
     uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int y = 0; y < 4; ++y) split2(__uint_as_float(x[y] << 16) * f, __uint_as_float(x[y] & 0xffff0000u) * f, hi[y], lo[y]);
+    for (int y = 0; y < 4; ++y)
+      split2<__NV_E4M3>(__uint_as_float(x[y] << 16) * f, __uint_as_float(x[y] & 0xffff0000u) * f, hi[y], lo[y]);
     *reinterpret_cast<uint2*>(d) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
     *reinterpret_cast<uint2*>(d + to_lo) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
   };
@@ -416,6 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
   uint64_t* mma_done = p_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  float* sUnit = reinterpret_cast<float*>(smem + C::OFF_MISC + 8);
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const bool packed = p.idx == nullptr;        // units are sequences
@@ -592,6 +610,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
       s_cur[u] = scale_of(checked_row(ip[u]));
       ip[u] = load_idx(slot0 + kN + lane + 32 * u);
     }
+    // Scales count in units of the first key's (of the first 32 slots, or the
+    // chunk's largest; rows of a CTA share their first keys), so that how far
+    // l is from 1 does not depend on the scales but on their spread.
+    const uint32_t some = __ballot_sync(0xffffffffu, s_cur[0] > 0.f);
+    const uint32_t s0 =
+        some != 0u ? __shfl_sync(0xffffffffu, __float_as_uint(s_cur[0]), __ffs((int)some) - 1)
+                   : __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(s_cur[1], fmaxf(s_cur[2], s_cur[3]))));
+    const float unit = s0 >= 0x00800000u ? __uint_as_float(s0 & 0x7f800000u) : 1.f;
+    const float unit_log2 = (float)((int)(__float_as_uint(unit) >> 23) - 127);
+    if (lane == 0) *sUnit = unit;
     for (int j = 0; j < nchunks; ++j) {
       float s_next[4];
 #pragma unroll
@@ -607,8 +635,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
         const bool on = s > 0.f;
         float* par = sPar + pb * 3 * kN + lane + 32 * u;
         par[0] = p.scale_log2 * s;
-        par[kN] = on ? log2f(s) : -INFINITY;
-        par[2 * kN] = on ? 1.f / s : 0.f;
+        par[kN] = on ? log2f(s) - unit_log2 : -INFINITY;
+        par[2 * kN] = on ? fminf(unit / s, 3.0e38f) : 0.f;   // (finite: it may meet a P of zero)
         s_cur[u] = s_next[u];
       }
       mbar_arrive(&par_full[pb]);
@@ -620,7 +648,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     // 80 cycles an MMA, more than the tensor core
     if (nchunks > 0) {
       constexpr uint32_t idesc_qk = make_idesc(kFmtE4M3, kFmtE4M3, 0, 0, kM, kN);
-      constexpr uint32_t idesc_pv = make_idesc(kFmtE4M3, kFmtE4M3, 0, 1, kM, C::NV);
+      constexpr uint32_t idesc_pv_hi = make_idesc(kFmtE4M3, kFmtE4M3, 0, 1, kM, C::NV);
+      constexpr uint32_t idesc_pv_lo = make_idesc(kFmtE5M2, kFmtE4M3, 0, 1, kM, C::NV);
       const uint64_t kdesc0 = make_sdesc(smem_u32(sKV), 16, 1024, kSwizzle128);
       const uint64_t ktail0 = make_sdesc(smem_u32(sKV) + C::NF * C::ATOM, 16, 512, kSwizzle64);
       const uint64_t qdesc0 = make_sdesc(smem_u32(sQ), 16, 1024, kSwizzle128);
@@ -682,8 +711,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
             for (int nv = 0; nv < C::NMMV; ++nv) {
               const uint64_t bdesc = vst + (uint64_t)((nv * (C::NV / 128) * C::ATOM + ks * 32 * 128) >> 4);
               const uint32_t dO = tmem + C::OCOL + nv * (C::NV / 2);
-              mma_ws<0>(dO, pst + (uint64_t)((ks * 32) >> 4), bdesc, idesc_pv, (pv > 0 || ks > 0) ? 1u : 0u);
-              mma_ws<1>(dO, pst + (uint64_t)((C::PTERM + ks * 32) >> 4), bdesc, idesc_pv, 1u);
+              mma_ws<0>(dO, pst + (uint64_t)((ks * 32) >> 4), bdesc, idesc_pv_hi,
+                        (pv > 0 || ks > 0) ? 1u : 0u);
+              mma_ws<1>(dO, pst + (uint64_t)((C::PTERM + ks * 32) >> 4), bdesc, idesc_pv_lo, 1u);
             }
             if (ks & 1) mma_commit(&kv_empty[2 * rg + ks / 2]);
           }
@@ -747,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
       if (lane == 0) mbar_arrive(q_ready);
     }
     bar_sync(4, 256);                                    // the staged terms are read: the P buffers are free
-    float R = -INFINITY, l = 0.f;                        // l: this thread's keys' share of the row sum
+    float R = -INFINITY, R_top = -INFINITY, l = 0.f;     // l: this thread's keys' share of the row sum
     bool ok = true;
     // a failed wait leaves the loop running without waits: the warps of a
     // barrier all arrive
@@ -794,9 +824,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
       float Rn = R;
       if (R == -INFINITY) {
         if (m != -INFINITY) Rn = m - kHead;
-      } else if (m - kHead > R + kSlack) {
+      } else if (m > R + kTop) {
         Rn = m - kHead;
+      } else if (slot1 - slot0 > kLongPart && m < R + (kHead - kDrop) && m != -INFINITY) {
+        Rn = fmaxf(m - kHead, R_top - kDepth);
       }
+      R_top = fmaxf(R_top, Rn);
       const bool moved = R != -INFINITY && Rn != R;
       const float alpha = moved ? exp2f(R - Rn) : 1.f;
       l *= alpha;
@@ -819,8 +852,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
           rs0 = fma2(pair2(e0, e1), iv.x, rs0);
           rs1 = fma2(pair2(e2, e3), iv.y, rs1);
           uint32_t h0, l0, h1, l1;
-          split2(e0, e1, h0, l0);
-          split2(e2, e3, h1, l1);
+          split2<__NV_E5M2>(e0, e1, h0, l0);
+          split2<__NV_E5M2>(e2, e3, h1, l1);
           hw[i] = h0 | (h1 << 16);
           lw[i] = l0 | (l1 << 16);
         }
@@ -869,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     const size_t orow = (p.nsplit == 1 ? (size_t)unit : (size_t)unit * p.nsplit + split) * p.HR;
     if (ok && nchunks > 0) {
       tc_fence_after();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = l > 0.f ? *sUnit / l : 0.f;
       constexpr int W = TC < 32 ? 16 : 32;
       // TMEM column x of the accumulator: MMA x / (NV/2), its columns
       // [kg NV/2, + NV/2) in this lane half; a thread's columns are in one MMA

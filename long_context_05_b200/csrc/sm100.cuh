@@ -315,7 +315,8 @@ __host__ __device__ constexpr uint32_t make_idesc(uint32_t a_fmt, uint32_t b_fmt
          ((M >> 4) << 24);
 }
 
-constexpr uint32_t kFmtE4M3 = 0, kFmtBF16 = 1;
+constexpr uint32_t kFmtE4M3 = 0, kFmtE5M2 = 1;   // kind::f8f6f4
+constexpr uint32_t kFmtBF16 = 1;                 // kind::f16
 
 // ------------------------------------------------------------------ cp.async
 
