@@ -348,7 +348,7 @@ dsa_status run_select(const LaunchCtx& c, const dsa_shape* s, const WsLayout& L,
 // dense_rows read keys 0..pos(t) and the rest read idx.
 dsa_status run_attn(const LaunchCtx& c, const dsa_shape* s, const uint16_t* q, const uint16_t* kv,
                     const uint16_t* v, const int32_t* idx, int dense_rows, uint16_t* out, float* lse, float* part,
-                    int nsplit) {
+                    int nsplit, bool after_selection) {
   AttnArgs a = {};
   a.map = kv_map(s);
   a.q = q; a.kv = kv; a.v = v; a.idx = idx; a.dense_rows = dense_rows;
@@ -357,6 +357,7 @@ dsa_status run_attn(const LaunchCtx& c, const dsa_shape* s, const uint16_t* q, c
   a.nsplit = nsplit;
   a.tau = tau_of(s);
   a.decode = s->mode == DSA_DECODE;
+  a.after_selection = after_selection;
   if (a.decode && attn_decode_supported(a)) return from_cuda(launch_sparse_attn_decode(c, a, part));
   return from_cuda(launch_sparse_attn(c, a));
 }
@@ -502,7 +503,7 @@ dsa_status dsa_sparse_attn(const dsa_shape* s, const uint16_t* q, const uint16_t
     if (ws == nullptr || ws_bytes < L.total) return DSA_ERR_WORKSPACE;
     part = reinterpret_cast<float*>(static_cast<char*>(ws) + L.part_off);
   }
-  return run_attn(c, s, q, kv, v, idx, 0, out, lse, part, L.nsplit);
+  return run_attn(c, s, q, kv, v, idx, 0, out, lse, part, L.nsplit, false);
 }
 
 dsa_status dsa_dense_attn(const dsa_shape* s, const uint16_t* q, const uint16_t* kv, const uint16_t* v,
@@ -519,7 +520,7 @@ dsa_status dsa_dense_attn(const dsa_shape* s, const uint16_t* q, const uint16_t*
     if (ws == nullptr || ws_bytes < L.total) return DSA_ERR_WORKSPACE;
     part = reinterpret_cast<float*>(static_cast<char*>(ws) + L.part_off);
   }
-  return run_attn(c, s, q, kv, v, nullptr, 0, out, lse, part, L.nsplit_dense);
+  return run_attn(c, s, q, kv, v, nullptr, 0, out, lse, part, L.nsplit_dense, false);
 }
 
 dsa_status dsa_forward(const dsa_shape* s, const dsa_inputs* in, uint16_t* out, float* lse, int32_t* idx_out,
@@ -548,7 +549,7 @@ dsa_status dsa_forward(const dsa_shape* s, const dsa_inputs* in, uint16_t* out, 
         DSA_OK)
       return st;
   }
-  return run_attn(c, s, in->q, in->kv, in->v, idx_out, d_rows, out, lse, part, L.nsplit);
+  return run_attn(c, s, in->q, in->kv, in->v, idx_out, d_rows, out, lse, part, L.nsplit, true);
 }
 
 dsa_status dsa_prefill(const dsa_shape* s, const dsa_inputs* in, uint16_t* out, float* lse, int32_t* idx_out,

@@ -147,6 +147,7 @@ struct AttnArgs {
   int nsplit;          // key splits per query row (1 = write out directly)
   float tau;
   bool decode;         // decode mode: the split-k memory-bound kernel where it applies
+  bool after_selection;  // the launch before this one is the path's top-k (its inputs are older)
 };
 
 // attention over an 8-bit cache (attn8.cu)
@@ -189,8 +190,9 @@ cudaError_t grant_smem(Kernel kernel, int bytes, int device, std::atomic<int>* g
 }
 
 // Launch with programmatic stream serialization: the kernel may start while
-// the one before it on the stream finishes, and must call pdl_wait
-// (sm100.cuh) before it reads anything that kernel writes.
+// the one before it on the stream, and through that one others before it,
+// still run, and must call pdl_wait (sm100.cuh) before it reads or writes
+// anything that one of them may touch.
 template <class... KArgs, class... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                        Args... args) {

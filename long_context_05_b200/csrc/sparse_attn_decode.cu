@@ -88,6 +88,7 @@ struct DecParams {
   float* part_lse;      // [rows, nsplit, H], log2 units
   int T, H, k;
   int rows, nsplit;
+  bool after_selection; // the launch before this one is the path's top-k
   float scale_log2;     // tau * log2(e)
   long long wait_ns;
   DevErr* err;
@@ -104,6 +105,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // the combine kernel may be scheduled now; it waits for this grid's results
   pdl_launch_dependents();
+  // Nothing of global memory is read before the kernel in front is done: it
+  // may be one that writes q or the lengths and has let this one start early.
+  // In the path that kernel is the top-k, behind an indexer launched the
+  // ordinary way, so q and the lengths are there, and only the selection is
+  // waited for, below.
+  if (!p.after_selection) pdl_wait();
   uint8_t* sQ = smem + OFF_Q;
   uint8_t* sKV = smem + OFF_KV;
   uint64_t* sMask = reinterpret_cast<uint64_t*>(smem + OFF_MASK);
@@ -557,6 +564,7 @@ cudaError_t launch_sparse_attn_decode(const LaunchCtx& c, const AttnArgs& a, voi
   p.k = a.k;
   p.rows = (int)rows;
   p.nsplit = attn_decode_nsplit(a.k);
+  p.after_selection = a.after_selection;
   p.scale_log2 = a.tau * 1.4426950408889634f;
   p.wait_ns = c.wait_ns;
   p.err = c.err;
@@ -572,8 +580,8 @@ cudaError_t launch_sparse_attn_decode(const LaunchCtx& c, const AttnArgs& a, voi
   auto kern = a.map.page_size != 0 ? sparse_attn_decode_kernel<true> : sparse_attn_decode_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  // a programmatic dependent of the top-k: its prologue overlaps the
-  // selection's last launch, which runs only one block per row
+  // a programmatic dependent: in the path its prologue overlaps the top-k's
+  // last launch, which runs only one block per row
   e = launch_pdl(kern, dim3((unsigned)(rows * p.nsplit)), dim3(kThreads), kSmem, c.stream, tm_q, p);
   if (e != cudaSuccess) return e;
   note_launches(1);
