@@ -168,25 +168,30 @@ struct Attn8Args {
 // counts every kernel launch (dsa_launch_count)
 void note_launches(int n);
 
-// Dynamic shared memory past what a kernel is allowed by itself: asked for
-// once per kernel and device (`granted`: the kernel's own array, bytes granted
-// so far), since asking costs a launch a fifth of its time.  `whole`: the
-// kernel runs with all of an SM's memory as shared memory, not what one wave
-// of it needs.
+// Dynamic shared memory past what a kernel is allowed by itself: all that the
+// device has, asked for once per kernel and device (`granted`: the kernel's own
+// array, bytes granted), since asking costs a launch a fifth of its time.  All
+// of it, whatever this call needs, so that threads with different needs ask
+// for the same and none takes back what another has been granted.  `whole`:
+// the kernel runs with all of an SM's memory as shared memory, not what one
+// wave of it needs.
 constexpr int kMaxDevices = 64;
 template <class Kernel>
 cudaError_t grant_smem(Kernel kernel, int bytes, int device, std::atomic<int>* granted, bool whole = false) {
-  if (bytes <= granted[device].load(std::memory_order_acquire)) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
-  if (whole) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  int have = granted[device].load(std::memory_order_acquire);
+  if (have == 0) {
+    cudaFuncAttributes fa;
+    cudaError_t e = cudaDeviceGetAttribute(&have, cudaDevAttrMaxSharedMemoryPerBlockOptin, device);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kernel);
     if (e != cudaSuccess) return e;
+    have -= (int)fa.sharedSizeBytes;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, have);
+    if (e == cudaSuccess && whole)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    granted[device].store(have, std::memory_order_release);
   }
-  int seen = granted[device].load(std::memory_order_relaxed);
-  while (seen < bytes && !granted[device].compare_exchange_weak(seen, bytes, std::memory_order_release)) {
-  }
-  return cudaSuccess;
+  return bytes <= have ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 // Launch with programmatic stream serialization: the kernel may start while
