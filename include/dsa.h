@@ -458,9 +458,10 @@ DSA_API size_t dsa_workspace8_size(const dsa_shape* shape);
  * probabilities split into an e4m3 and an e5m2 term (2^-8 of themselves, as
  * BF16 ones, and together at most 2^-9 of the largest product of a
  * probability and its row's scale, of more than 2048 keys of each 128 keys'
- * largest), accumulated in FP32; out is rounded to BF16 once.  The two modes give the same results; calls of
- * few rows split their keys over the SMs and need the workspace.  B T H is
- * below 2^31. */
+ * largest), accumulated in FP32; out is rounded to BF16 once.  A head row of
+ * q with a NaN or an infinity gives NaN in out and lse.  The two modes give
+ * the same results; calls of few rows split their keys over the SMs and need
+ * the workspace.  B T H is below 2^31. */
 DSA_API dsa_status dsa_sparse_attn8(const dsa_shape* shape, const uint16_t* q, const uint8_t* kv8,
                             const float* kv_scale, const int32_t* idx, uint16_t* out, float* lse, void* ws,
                             size_t ws_bytes, void* stream);

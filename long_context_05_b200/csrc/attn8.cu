@@ -366,9 +366,11 @@ __device__ __forceinline__ void split_q_rows(const QRows<DK, R>& q4, int r0, int
   float inv[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const int e = pow2_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, m[i]) << 16));
+    const uint32_t most = __reduce_max_sync(0xffffffffu, m[i]);
+    const int e = pow2_exponent(__uint_as_float(most << 16));
     inv[i] = __uint_as_float((uint32_t)(127 - e) << 23);
-    if (lane == i) sE[r0 + i] = __uint_as_float((uint32_t)(127 + e) << 23);
+    // a row with an infinity or a NaN has NaN logits (e4m3 has no infinity)
+    if (lane == i) sE[r0 + i] = most >= 0x7f80u ? __uint_as_float(0x7fffffffu) : __uint_as_float((uint32_t)(127 + e) << 23);
   }
   // both terms of eight columns: 8 bytes at d and at d + to_lo
   auto put = [&](const uint4& v, float f, uint8_t* d, int to_lo) {
@@ -902,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
     const size_t orow = (p.nsplit == 1 ? (size_t)unit : (size_t)unit * p.nsplit + split) * p.HR;
     if (ok && nchunks > 0) {
       tc_fence_after();
-      const float inv = l > 0.f ? *sUnit / l : 0.f;
+      const float inv = l == 0.f ? 0.f : *sUnit / l;    // (a NaN stays one)
       constexpr int W = TC < 32 ? 16 : 32;
       // TMEM column x of the accumulator: MMA x / (NV/2), its columns
       // [kg NV/2, + NV/2) in this lane half; a thread's columns are in one MMA
@@ -949,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
       }
     }
     if (ok && kg == 0 && c == 0 && head_ok) {
-      const float lse2 = l > 0.f ? R + log2f(l) : -INFINITY;
+      const float lse2 = l == 0.f ? -INFINITY : R + log2f(l);
       if (p.nsplit == 1) {
         if (p.lse != nullptr) p.lse[orow + h] = lse2 * 0.6931471805599453f;
       } else {
@@ -1004,9 +1006,11 @@ __global__ void __launch_bounds__(kCombineThreads, 6) attn8_combine_kernel(const
         po += H * DV;
       }
     }
+    // (a NaN part counts as no maximum but is added: the sum becomes NaN)
     const float m = fmaxf(mx, fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])));
-    if (m == -INFINITY) continue;
-    const float alpha = exp2f(mx - m);
+    const bool nan = isnan(l[0]) || isnan(l[1]) || isnan(l[2]) || isnan(l[3]);
+    if (m == -INFINITY && !nan) continue;
+    const float alpha = m == -INFINITY ? 1.f : exp2f(mx - m);
     mx = m;
     wsum *= alpha;
 #pragma unroll
@@ -1026,12 +1030,12 @@ __global__ void __launch_bounds__(kCombineThreads, 6) attn8_combine_kernel(const
       }
     }
   }
-  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
   *reinterpret_cast<uint4*>(out + (size_t)gh * DV + d0) = make_uint4(w[0], w[1], w[2], w[3]);
-  if (d0 == 0 && lse != nullptr) lse[gh] = wsum > 0.f ? (mx + log2f(wsum)) * 0.6931471805599453f : -INFINITY;
+  if (d0 == 0 && lse != nullptr) lse[gh] = wsum == 0.f ? -INFINITY : (mx + log2f(wsum)) * 0.6931471805599453f;
 }
 
 template <int DK, int DV, bool PAGED>

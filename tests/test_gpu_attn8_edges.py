@@ -1,0 +1,45 @@
+"""Attention over an 8-bit cache at the ends of its inputs' ranges, on the GPU."""
+import pytest
+import torch
+
+from long_context_05_b200 import dsa
+from tests.test_gpu_attn8 import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    dsa.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("B,T,H,d_k,k,dense,page", [
+    (1, 1, 128, 576, 600, False, 0),                   # a chunk to a part
+    (20, 1, 128, 576, 600, False, 16),                 # two chunks to a part
+    (1, 80, 128, 576, 600, False, 0),                  # one part
+    (1, 1, 24, 576, 8, True, 0),
+    (1, 100, 40, 576, 8, True, 0),                     # several queries to a CTA
+    (1, 1, 16, 80, 300, False, 0),
+    (1, 160, 128, 80, 300, False, 0),
+])
+def test_queries_that_are_no_numbers(bad, B, T, H, d_k, k, dense, page):
+    """NaN out and lse in the rows that hold one, split or not; the other rows as without them."""
+    c = Case(B, T, 700, H, d_k, k, page, seed=3)
+    if not dense:
+        c.select()
+    want = c.run(dense=dense)
+    rows = [(0, 0, 0), (B - 1, T - 1, H - 1), (0, T // 2, H // 2)]
+    for i, (b, t, h) in enumerate(rows):
+        c.q[b, t, h, (0, d_k - 1, 65)[i]] = bad
+    out, lse = c.run(dense=dense)
+    assert dsa.device_error()[0] == 0
+    hit = torch.zeros(B, T, H, dtype=torch.bool, device="cuda")
+    for r in rows:
+        hit[r] = True
+    assert bool(out[hit].isnan().all()) and bool(lse[hit].isnan().all())
+    assert torch.equal(out[~hit], want[0][~hit]) and torch.equal(lse[~hit], want[1][~hit])
