@@ -429,9 +429,9 @@ DSA_API dsa_status dsa_norm_rope_backward(const dsa_shape* shape, const dsa_norm
  * Each of the three parts may be left out (its three pointers NULL).
  * A row's scale is 2^e with the smallest e >= -48 for which
  * max|x| <= 448 * 2^e, its bytes are e4m3(x * 2^-e) rounded to nearest even
- * (values past 240 * 2^120 are stored as that; x holds no NaN).  Other rows of
- * the caches are left as they are; a row whose page is unmapped is reported and
- * dropped. */
+ * (values past 240 * 2^120 are stored as that; x holds no NaN; the attention
+ * below takes scales up to 2^100).  Other rows of the caches are left as they
+ * are; a row whose page is unmapped is reported and dropped. */
 DSA_API dsa_status dsa_cache_write(const dsa_shape* shape, const uint16_t* kv, uint8_t* kv8, float* kv_scale,
                            const uint16_t* k_I, uint8_t* kI8, float* kI_scale, const uint16_t* q_I, uint8_t* qI8,
                            float* qI_scale, void* stream);
@@ -451,17 +451,19 @@ DSA_API size_t dsa_workspace8_size(const dsa_shape* shape);
 
 /* Step C over an 8-bit cache: dsa_sparse_attn with key row s dequantised as
  * kv_scale[s] * e4m3(kv8[s]) (V = its first d_v columns).  kv8 [B, S, d_k]
- * bytes and kv_scale [B, S] FP32 (paged: pools of rows); any finite scales in
- * [2^-100, 2^100].  Selected rows hold no NaN bytes; other rows may hold
- * anything.  The products are those of the given bytes with q split into two
- * e4m3 terms (off by 2^-17.8 of the head row's largest at most) and with the
- * probabilities split into an e4m3 and an e5m2 term (2^-8 of themselves, as
- * BF16 ones, and together at most 2^-9 of the largest product of a
- * probability and its row's scale, of more than 2048 keys of each 128 keys'
- * largest), accumulated in FP32; out is rounded to BF16 once.  A head row of
- * q with a NaN or an infinity gives NaN in out and lse.  The two modes give
- * the same results; calls of few rows split their keys over the SMs and need
- * the workspace.  B T H is below 2^31. */
+ * bytes and kv_scale [B, S] FP32 (paged: pools of rows); scales in
+ * [2^-100, 2^100], of one query's keys within a factor of 2^64 of one another
+ * (a key's weight is formed from 2^logit times its scale: a key of a scale
+ * 2^130 below another's drops out of the sum).  Selected rows hold no NaN
+ * bytes; other rows may hold anything.  The products are those of the given
+ * bytes with q split into two e4m3 terms (off by 2^-17.8 of the head row's
+ * largest at most) and with the probabilities split into an e4m3 and an e5m2
+ * term (2^-8 of themselves, as BF16 ones, and together at most 2^-9 of the
+ * largest product of a probability and its row's scale, of more than 2048
+ * keys of each 128 keys' largest), accumulated in FP32; out is rounded to
+ * BF16 once.  A head row of q with a NaN or an infinity gives NaN in out and
+ * lse.  The two modes give the same results; calls of few rows split their
+ * keys over the SMs and need the workspace.  B T H is below 2^31. */
 DSA_API dsa_status dsa_sparse_attn8(const dsa_shape* shape, const uint16_t* q, const uint8_t* kv8,
                             const float* kv_scale, const int32_t* idx, uint16_t* out, float* lse, void* ws,
                             size_t ws_bytes, void* stream);

@@ -43,3 +43,13 @@ def test_queries_that_are_no_numbers(bad, B, T, H, d_k, k, dense, page):
         hit[r] = True
     assert bool(out[hit].isnan().all()) and bool(lse[hit].isnan().all())
     assert torch.equal(out[~hit], want[0][~hit]) and torch.equal(lse[~hit], want[1][~hit])
+
+
+@pytest.mark.parametrize("exps", [[-30.0, 34.0], [-100.0, -36.0], [36.0, 60.0, 100.0], [-64.0, 0.0]])
+@pytest.mark.parametrize("T,S,dense", [(1, 900, False), (80, 900, False), (3, 900, True), (80, 2900, True)])
+def test_scales_two_to_the_64_apart(T, S, dense, exps):
+    """Keys of about the same weight, whose scales are as far apart as they may be."""
+    c = Case(1, T, S, 128, 576, 700, exps=torch.tensor(exps, device="cuda"), tau=2.0 ** -(max(exps) + 10))
+    if not dense:
+        c.select()
+    c.check(*c.run(dense=dense), dense=dense, rows=sorted({0, T // 2, T - 1}))
