@@ -180,7 +180,7 @@ struct Params {
 __device__ __forceinline__ int pow2_exponent(float amax) {
   const uint32_t u = __float_as_uint(amax);
   const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return min(max(e, -100), 120);
+  return min(max(e, -126), 120);
 }
 template <__nv_fp8_interpretation_t TO>
 __device__ __forceinline__ uint32_t fp8x2_of_half2(__half2 h) {
@@ -801,8 +801,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const ulonglong2 a = par[i], lg = par[kN / 4 + i];
-        x[2 * i] = fma2(mul2(pair2u(s[4 * i], s[4 * i + 1]), f2), a.x, lg.x);
-        x[2 * i + 1] = fma2(mul2(pair2u(s[4 * i + 2], s[4 * i + 3]), f2), a.y, lg.y);
+        // (the row's power of two meets the key's scale first: with the sum
+        // first, 2^112 and more of it overflowed before a small scale came)
+        x[2 * i] = fma2(pair2u(s[4 * i], s[4 * i + 1]), mul2(a.x, f2), lg.x);
+        x[2 * i + 1] = fma2(pair2u(s[4 * i + 2], s[4 * i + 3]), mul2(a.y, f2), lg.y);
       }
       const int past = last - (slot0 + j * kN + kg * 64 + c * 32);   // keys i > past are not this row's
       if (__any_sync(0xffffffffu, past < 31)) {

@@ -53,3 +53,13 @@ def test_scales_two_to_the_64_apart(T, S, dense, exps):
     if not dense:
         c.select()
     c.check(*c.run(dense=dense), dense=dense, rows=sorted({0, T // 2, T - 1}))
+
+
+@pytest.mark.parametrize("T", [1, 80])
+@pytest.mark.parametrize("size,exps,tau", [(118, [-100.0, -99.0], 2.0 ** -30), (-108, [99.0, 100.0], 2.0 ** -4),
+                                           (-116, [99.0, 100.0], 2.0 ** 4)])
+def test_queries_near_the_ends_of_bf16(T, size, exps, tau):
+    """Queries far from one beside scales that bring their logits back."""
+    c = Case(1, T, 300, 128, 576, 200, exps=torch.tensor(exps, device="cuda"), tau=tau).select()
+    c.q *= 2.0 ** size
+    c.check(*c.run(), rows=[0, T - 1])
