@@ -401,7 +401,9 @@ typedef struct {
  *   z_c = weight_c x_c / sqrt(mean_{c < norm_cols} x_c^2 + eps) for
  *   c < norm_cols, x_c past them; the last rope_cols columns of z are rotated
  *   in pairs (a, b) -> (a cos - b sin, a sin + b cos) by pos(t) inv_freq_i
- *   (the angle is formed in FP64); rounded to BF16 once. */
+ *   (the angle is formed in FP64); rounded to BF16 once.  The squares are FP32:
+ *   rows whose normalised columns' sum of squares passes 2^128, or whose mean
+ *   square plus eps is below 2^-126, lose them (zeros; infinities and NaN). */
 DSA_API dsa_status dsa_norm_rope(const dsa_shape* shape, const dsa_norm_rope_desc* desc, const uint16_t* q,
                          const uint16_t* k, uint16_t* q_out, uint16_t* k_out, void* stream);
 

@@ -364,7 +364,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(V, BACK, MODE == kHalf
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const float h = rsqrtf(fmaf(ss[u], p.inv_norm, p.eps));
-        const float c = -(h * h * h * dot[u] * p.inv_norm);
+        // (in this order no step passes FP32: h^3 alone does for rows of 1e-13)
+        const float c = -(dot[u] * p.inv_norm * h * h * h);
         rho[u] = pair(h, h);
         c1[u] = pair(c, c);
         dst[u] = reinterpret_cast<uint4*>((BACK ? s.dx : s.y) + (size_t)(row0 + r[u]) * p.D) + gl;
