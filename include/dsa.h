@@ -433,7 +433,8 @@ DSA_API dsa_status dsa_norm_rope_backward(const dsa_shape* shape, const dsa_norm
  * max|x| <= 448 * 2^e, its bytes are e4m3(x * 2^-e) rounded to nearest even
  * (values past 240 * 2^120 are stored as that; x holds no NaN; the attention
  * below takes scales up to 2^100).  Other rows of the caches are left as they
- * are; a row whose page is unmapped is reported and dropped. */
+ * are; a row whose page is unmapped, and the rows of a sequence shorter than T,
+ * are reported and dropped. */
 DSA_API dsa_status dsa_cache_write(const dsa_shape* shape, const uint16_t* kv, uint8_t* kv8, float* kv_scale,
                            const uint16_t* k_I, uint8_t* kI8, float* kI_scale, const uint16_t* q_I, uint8_t* qI8,
                            float* qI_scale, void* stream);

@@ -129,11 +129,14 @@ struct WriteParams {
   DevErr* err;
 };
 
-// Cache row of new token n (position L_b - T + t); -1 for an unmapped page.
+// Cache row of new token n (position L_b - T + t); -1 for an unmapped page and
+// for a sequence shorter than its new tokens (an empty slot of a batch: the
+// first rows, or what its stale page table names, may be another's).
 template <bool PAGED>
 __device__ __forceinline__ long long new_row(const KvMap& map, int n, int T, DevErr* err, bool report) {
   const int b = n / T, t = n - b * T;
   const int pos = map.len(b, report ? err : nullptr, ERR_SITE_CACHE) - T + t;
+  if (map.seqlens != nullptr && map.seqlens[b] < T) return -1;   // (reported by len)
   const long long r = map.row<PAGED>(b, pos);
   if (r < 0 && report) report_error(err, DSA_ERR_DEVICE_BOUNDS, ERR_SITE_CACHE | (1u << 8));
   return r;
