@@ -63,3 +63,12 @@ def test_queries_near_the_ends_of_bf16(T, size, exps, tau):
     c = Case(1, T, 300, 128, 576, 200, exps=torch.tensor(exps, device="cuda"), tau=tau).select()
     c.q *= 2.0 ** size
     c.check(*c.run(), rows=[0, T - 1])
+
+
+def test_dense_rows_in_front_of_unfinished_ones():
+    """Keys past a query's own position are not read where a CTA holds one query: its results are those of its keys."""
+    c = Case(1, 40, 100, 64, 576, 8)
+    c.kv8[90:] = 0x7F
+    c.scale[90:] = float("inf")
+    out, lse = c.run(dense=True)
+    c.check(out[:, :30].contiguous(), lse[:, :30].contiguous(), dense=True, rows=[0, 1, 15, 28, 29])
