@@ -84,38 +84,18 @@ struct NrParams {
 struct F8 {
   uint64_t v[4];
 };
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 __device__ __forceinline__ F8 unpack8(const uint4& v) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
   F8 f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) f.v[i] = pair(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+  for (int i = 0; i < 4; ++i) f.v[i] = pair2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
   return f;
 }
 __device__ __forceinline__ uint4 pack8(const F8& f) {
   uint32_t u[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 x = unpair(f.v[i]);
+    const float2 x = unpair2(f.v[i]);
     u[i] = pack_bf16x2(x.x, x.y);
   }
   return make_uint4(u[0], u[1], u[2], u[3]);
@@ -160,9 +140,9 @@ __device__ __forceinline__ void rotate8(F8& z, const F8& o, const float2* cs, in
   if constexpr (MODE == kInter) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 a = cs[(rc >> 1) + i], z2 = unpair(z.v[i]);
+      const float2 a = cs[(rc >> 1) + i], z2 = unpair2(z.v[i]);
       const float s = back ? -a.y : a.y;
-      z.v[i] = pair(z2.x * a.x - z2.y * s, z2.x * s + z2.y * a.x);
+      z.v[i] = pair2(z2.x * a.x - z2.y * s, z2.x * s + z2.y * a.x);
     }
   } else if constexpr (MODE == kHalf) {
     const bool first = rc < half;
@@ -171,7 +151,7 @@ __device__ __forceinline__ void rotate8(F8& z, const F8& o, const float2* cs, in
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float4 a = a0[i];                     // two angles
-      z.v[i] = fma2(o.v[i], pair(a.y * sign, a.w * sign), mul2(z.v[i], pair(a.x, a.z)));
+      z.v[i] = fma2(o.v[i], pair2(a.y * sign, a.w * sign), mul2(z.v[i], pair2(a.x, a.z)));
     }
   }
 }
@@ -348,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(V, BACK, MODE == kHalf
       float ss[U], dot[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const float2 a = unpair(ss2[u]), d = unpair(dot2[u]);
+        const float2 a = unpair2(ss2[u]), d = unpair2(dot2[u]);
         ss[u] = a.x + a.y;
         dot[u] = d.x + d.y;
       }
@@ -366,8 +346,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(V, BACK, MODE == kHalf
         const float h = rsqrtf(fmaf(ss[u], p.inv_norm, p.eps));
         // (in this order no step passes FP32: h^3 alone does for rows of 1e-13)
         const float c = -(dot[u] * p.inv_norm * h * h * h);
-        rho[u] = pair(h, h);
-        c1[u] = pair(c, c);
+        rho[u] = pair2(h, h);
+        c1[u] = pair2(c, c);
         dst[u] = reinterpret_cast<uint4*>((BACK ? s.dx : s.y) + (size_t)(row0 + r[u]) * p.D) + gl;
       }
       // dx at normalised columns, from g and x; the weight sums
@@ -455,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(V, BACK, MODE == kHalf
     for (int j = 0; j < V; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float2 two = unpair(acc[j].v[i / 2]);
+        const float2 two = unpair2(acc[j].v[i / 2]);
         float a = i & 1 ? two.y : two.x;
 #pragma unroll
         for (int d = G; d < 32; d <<= 1) a += __shfl_xor_sync(0xffffffffu, a, d);
