@@ -94,7 +94,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kHead = 6.f;           // log2 of the largest P of a row when R is set (P is then exact)
 constexpr float kTop = 8.75f;          // ... and at most (2^8.75 < 448)
 // (With kHead 4, 5, 6 and 8, on keys of spread norms, R moves in 9.1, 9.7, 10.4
-// and 12.3 of 15 chunks of a warp: 1311, 1314 and 1320 us with 4, 5 and 6 on
+// and 12.3 of 15 chunks of a warp: 1114, 1119 and 1123 us with 4, 5 and 6 on
 // 2048 queries of 128 heads over 2048 keys.)
 constexpr float kDrop = 4.f;           // how far a chunk's maximum may fall short of kHead
 constexpr int kLongPart = 2048;        // in parts of more keys than this
@@ -581,22 +581,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
       s_cur[u] = scale_of(checked_row(ip[u]));
       ip[u] = load_idx(slot0 + kN + lane + 32 * u);
     }
-    // Scales count in units of the first key's (of the first 32 slots, or the
-    // chunk's largest; rows of a CTA share their first keys), so that how far
-    // l is from 1 does not depend on the scales but on their spread.
-    const uint32_t some = __ballot_sync(0xffffffffu, s_cur[0] > 0.f);
-    const uint32_t s0 =
-        some != 0u ? __shfl_sync(0xffffffffu, __float_as_uint(s_cur[0]), __ffs((int)some) - 1)
-                   : __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(s_cur[1], fmaxf(s_cur[2], s_cur[3]))));
-    const float unit = s0 >= 0x00800000u ? __uint_as_float(s0 & 0x7f800000u) : 1.f;
-    const float unit_log2 = (float)((int)(__float_as_uint(unit) >> 23) - 127);
-    if (lane == 0) *sUnit = unit;
+    float unit = 1.f, unit_log2 = 0.f;
     for (int j = 0; j < nchunks; ++j) {
       float s_next[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         s_next[u] = scale_of(checked_row(ip[u]));
         ip[u] = load_idx(slot0 + (j + 2) * kN + lane + 32 * u);
+      }
+      if (j == 0) {
+        // Scales count in units of the first key's (of the first 32 slots, or
+        // the chunk's largest; rows of a CTA share their first keys), so that
+        // how far l is from 1 does not depend on the scales but on their spread.
+        const uint32_t some = __ballot_sync(0xffffffffu, s_cur[0] > 0.f);
+        const uint32_t s0 =
+            some != 0u ? __shfl_sync(0xffffffffu, __float_as_uint(s_cur[0]), __ffs((int)some) - 1)
+                       : __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(s_cur[1], fmaxf(s_cur[2], s_cur[3]))));
+        if (s0 >= 0x00800000u) unit = __uint_as_float(s0 & 0x7f800000u);
+        unit_log2 = (float)((int)(__float_as_uint(unit) >> 23) - 127);
+        if (lane == 0) *sUnit = unit;
       }
       const int pb = j & 1;
       if (j >= 2 && !wwait(&par_empty[pb], (uint32_t)(j / 2 - 1) & 1)) { fail(3); break; }
@@ -757,23 +760,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
       const uint32_t ph = (uint32_t)(j / 2) & 1;
       // 1. 32 scaled logits and their maximum
       if (ok && !wwait(&par_full[pb], ph)) { fail(7); ok = false; }
-      if (ok && !wwait(&s_full[pb], ph)) { fail(8); ok = false; }
-      tc_fence_after();
-      uint32_t s[32];
-      tmem_ld32(tmem + lane_addr + C::SCOL + pb * (kN / 2) + c * 32, s);
-      tmem_wait_ld_dep(s);
-      // (two keys an instruction where FP32 comes packed)
+      // (two keys an instruction where FP32 comes packed; the row's power of two
+      // meets the key's scale, while q K^T runs, before it meets the sum, which
+      // with 2^102 and more of it would overflow in front of a small scale)
       const ulonglong2* par = reinterpret_cast<const ulonglong2*>(sPar + pb * 3 * kN + kg * 64 + c * 32);
       const uint64_t f2 = pair2(f_h, f_h);
       uint64_t x[16];
       float cm = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const ulonglong2 a = par[i], lg = par[kN / 4 + i];
-        // (the row's power of two meets the key's scale first: with the sum
-        // first, 2^112 and more of it overflowed before a small scale came)
-        x[2 * i] = fma2(pair2u(s[4 * i], s[4 * i + 1]), mul2(a.x, f2), lg.x);
-        x[2 * i + 1] = fma2(pair2u(s[4 * i + 2], s[4 * i + 3]), mul2(a.y, f2), lg.y);
+        const ulonglong2 a = par[i];
+        x[2 * i] = mul2(a.x, f2);
+        x[2 * i + 1] = mul2(a.y, f2);
+      }
+      if (ok && !wwait(&s_full[pb], ph)) { fail(8); ok = false; }
+      tc_fence_after();
+      uint32_t s[32];
+      tmem_ld32(tmem + lane_addr + C::SCOL + pb * (kN / 2) + c * 32, s);
+      tmem_wait_ld_dep(s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const ulonglong2 lg = par[kN / 4 + i];
+        x[2 * i] = fma2(pair2u(s[4 * i], s[4 * i + 1]), x[2 * i], lg.x);
+        x[2 * i + 1] = fma2(pair2u(s[4 * i + 2], s[4 * i + 3]), x[2 * i + 1], lg.y);
       }
       const int past = last - (slot0 + j * kN + kg * 64 + c * 32);   // keys i > past are not this row's
       if (__any_sync(0xffffffffu, past < 31)) {
@@ -794,15 +803,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn8_kernel(Params p) {
       mx[(kg * 2 + c) * kM] = cm;
       bar_sync(2 + (quarter & 1), 128);
       const float m = fmaxf(fmaxf(mx[0], mx[kM]), fmaxf(mx[2 * kM], mx[3 * kM]));
-      float Rn = R;
-      if (R == -INFINITY) {
-        if (m != -INFINITY) Rn = m - kHead;
-      } else if (m > R + kTop) {
-        Rn = m - kHead;
-      } else if (slot1 - slot0 > kLongPart && m < R + (kHead - kDrop) && m != -INFINITY) {
-        Rn = fmaxf(m - kHead, R_top - kDepth);
+      float Rn = m > R + kTop ? m - kHead : R;
+      if (slot1 - slot0 > kLongPart) {
+        if (m < R + (kHead - kDrop) && m != -INFINITY) Rn = fmaxf(m - kHead, R_top - kDepth);
+        R_top = fmaxf(R_top, Rn);
       }
-      R_top = fmaxf(R_top, Rn);
       const bool moved = R != -INFINITY && Rn != R;
       const float alpha = moved ? exp2f(R - Rn) : 1.f;
       l *= alpha;
