@@ -62,19 +62,22 @@
 // through shared memory.  When R moves, the accumulator is rescaled once.
 //
 // Measured (576 / 512).  2048 queries of 128 heads over 2048 selected keys
-// each: 1106 us, 1056 TFLOP/s of the 1168 GFLOP counted once (the two terms
-// count double on the tensor cores); kept up for seconds, 1280 us at the
-// board's power limit.  Two chunks take 7400 cycles of a CTA: the MMAs 6475,
-// and 925 of waiting for the second chunk's softmax, which is longer than the
-// P V it runs under.  To its first logits a CTA takes about 10000 cycles, 5500 of
-// them until q and the first chunk are there (150 KB at 27 bytes a clock from
-// L2 with every SM asking; a third fewer instructions in q's split changed
-// nothing), for its output 3500 (the stores' way out).  Sixteen
-// softmax warps were slower (1575 us: the MMA warp lost issue slots), and so
-// were CTAs that stay and place the next tile's q under the end of the last
-// (1150 us for 1160 then, but dense calls 515 for 444: the hardware's own
-// order of unequal CTAs is better, and the split slows the output down).  A
-// decode step of 8 x 128 heads over 2048 keys: 17.2 us with the combine.
+// each: 1290 to 1320 us kept up for seconds, at the board's power limit (885 to
+// 905 TFLOP/s of the 1168 GFLOP counted once; the two terms count double on
+// the tensor cores), 1120 us back to back before it sets in.  A CTA takes
+// 72800 cycles, and the next 1400 more to start.  To its first logits 10300,
+// 7900 of them until q lies in place (150 KB of q and keys at 27 bytes a clock
+// from L2 with every SM asking; a third fewer instructions in q's split
+// changed nothing); then 7400 for two chunks, with keys of one norm 6475 of
+// MMAs and 925 of waiting for the second chunk's softmax, which is longer than
+// the P V it runs under; from the last P V to the last store 2500 (the stores'
+// way out), and 1100 to its end.  Sixteen softmax warps were slower (1575 us:
+// the MMA warp lost issue slots), and so were CTAs that stay and place the
+// next tile's q under the end of the last (1150 us for 1160 then, but dense
+// calls 515 for 444: the hardware's own order of unequal CTAs is better, and
+// the split slows the output down).  A decode step of 8 x 128 heads over 2048
+// keys: 16.8 us with the combine.  A selection leaves a CTA the heads of one
+// query: with 8 heads an eighth of its rows is used, with 72 nine in sixteen.
 #include <cuda_fp8.h>
 #include <math.h>
 
