@@ -1067,10 +1067,14 @@ size_t part_bytes(const Plan& p, int d_v) {
 
 }  // namespace
 
-// Workspace of the attention over an 8-bit cache, for sparse and dense calls.
+// Workspace of the attention over an 8-bit cache: of a sparse or a dense call,
+// and of either.
+size_t attn8_call_bytes(const Attn8Args& a, bool dense, int num_sms) {
+  return (part_bytes(plan(a, dense, num_sms), a.d_v) + 255) / 256 * 256;
+}
 size_t attn8_workspace_bytes(const Attn8Args& a, int num_sms) {
-  const size_t s = part_bytes(plan(a, false, num_sms), a.d_v), d = part_bytes(plan(a, true, num_sms), a.d_v);
-  return ((s > d ? s : d) + 255) / 256 * 256;
+  const size_t s = attn8_call_bytes(a, false, num_sms), d = attn8_call_bytes(a, true, num_sms);
+  return s > d ? s : d;
 }
 
 cudaError_t launch_attn8(const LaunchCtx& c, const Attn8Args& a) {

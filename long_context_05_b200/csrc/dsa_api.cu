@@ -378,7 +378,7 @@ dsa_status run_attn8(const LaunchCtx& c, const dsa_shape* s, const uint16_t* q, 
                      const float* kv_scale, const int32_t* idx, int dense_rows, uint16_t* out, float* lse, void* ws,
                      size_t ws_bytes) {
   Attn8Args a = attn8_args(s);
-  const size_t need = attn8_workspace_bytes(a, c.num_sms);
+  const size_t need = attn8_call_bytes(a, idx == nullptr, c.num_sms);
   if (need > 0 && (ws == nullptr || ws_bytes < need)) return DSA_ERR_WORKSPACE;
   a.q = q; a.kv8 = kv8; a.kv_scale = kv_scale; a.idx = idx; a.dense_rows = dense_rows;
   a.out = out; a.lse = lse; a.ws = ws;

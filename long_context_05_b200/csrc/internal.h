@@ -256,7 +256,9 @@ cudaError_t launch_indexer_bwd_tc(const LaunchCtx& c, const KvMap& map, const ui
                                   int q_count, float* dq, float* dw, float* dk);
 
 cudaError_t launch_attn8(const LaunchCtx& c, const Attn8Args& a);
-// scratch of launch_attn8 for the shape in `a` (pointers not read), sparse or dense
+// scratch of launch_attn8 for the shape in `a` (pointers not read): of a sparse
+// or a dense call, and of either
+size_t attn8_call_bytes(const Attn8Args& a, bool dense, int num_sms);
 size_t attn8_workspace_bytes(const Attn8Args& a, int num_sms);
 
 cudaError_t launch_wait_timeout_probe(const LaunchCtx& c);

@@ -72,3 +72,19 @@ def test_dense_rows_in_front_of_unfinished_ones():
     c.scale[90:] = float("inf")
     out, lse = c.run(dense=True)
     c.check(out[:, :30].contiguous(), lse[:, :30].contiguous(), dense=True, rows=[0, 1, 15, 28, 29])
+
+
+@pytest.mark.parametrize("B,T,H,dense", [(1, 160, 8, False), (2, 100, 24, False), (3, 80, 64, True)])
+def test_calls_of_many_rows_need_no_workspace(B, T, H, dense):
+    """Enough rows for every SM in this call, few in the other kind's: nothing is split, so nothing is asked for."""
+    c = Case(B, T, 300, H, 576, 100)
+    if not dense:
+        c.select()
+    want = c.run(dense=dense)
+    out, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    if dense:
+        dsa.dense_attn8(c.shape, c.q, c.kv8, c.scale, out, lse, None)
+    else:
+        dsa.sparse_attn8(c.shape, c.q, c.kv8, c.scale, c.idx, out, lse, None)
+    assert dsa.device_error()[0] == 0
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
