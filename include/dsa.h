@@ -414,8 +414,8 @@ DSA_API size_t dsa_norm_rope_workspace_size(const dsa_shape* shape, const dsa_no
  * NULL when norm_cols is 0) and the gradients dq_out, dk_out of its outputs,
  * dq, dk BF16 (dq_out's and dk_out's own buffers are allowed) and the norm
  * weights' dq_weight, dk_weight FP32 [norm_cols] (written, not added to, zeros
- * for a side without heads; NULL: not wanted).  The weight sums run in a fixed
- * order.
+ * for a side without heads; NULL: not wanted).  The weight sums are FP32 and
+ * run in a fixed order.
  * ws: dsa_norm_rope_workspace_size bytes (may be NULL when no weight gradient
  * is wanted). */
 DSA_API dsa_status dsa_norm_rope_backward(const dsa_shape* shape, const dsa_norm_rope_desc* desc, const uint16_t* q,
@@ -466,7 +466,9 @@ DSA_API size_t dsa_workspace8_size(const dsa_shape* shape);
  * keys of each 128 keys' largest), accumulated in FP32; out is rounded to
  * BF16 once.  A head row of q with a NaN or an infinity gives NaN in out and
  * lse.  The two modes give the same results; calls of few rows split their
- * keys over the SMs and need the workspace.  B T H is below 2^31. */
+ * keys over the SMs and need the workspace, where the parts' outputs lie in
+ * FP16 with an FP32 factor for every 32 columns (2^-11 of themselves).  B T H
+ * is below 2^31. */
 DSA_API dsa_status dsa_sparse_attn8(const dsa_shape* shape, const uint16_t* q, const uint8_t* kv8,
                             const float* kv_scale, const int32_t* idx, uint16_t* out, float* lse, void* ws,
                             size_t ws_bytes, void* stream);
